@@ -146,6 +146,45 @@ tv_status tv_kv_append_rope(const void* k_new, const void* v_new,
                             uint32_t* err, void* stream);
 
 /*
+ * tv_kv_append_mrope -- the append of tokens that stand at a position on each
+ * of several axes (time, height, width of an image or video; a text token
+ * stands at the same position on every axis), with q rotated in the same
+ * launch.  The source pages know positions on one axis only; the reading:
+ *   - pair (i, i + head_dim/2) of every q and K head turns by the angle of
+ *     positions[pair_axis[i]] in the table of tv_kv_append_rope, with that
+ *     call's pairing and arithmetic (num_axes = 1 gives its result);
+ *   - contiguous sections and interleaved axes are both a pair_axis array.
+ *   q_out         [num_tokens][num_q_heads][head_dim] bf16, written: the
+ *                 rotated q; NULL together with q rotates K alone
+ *   q, k_new, v_new  bf16; token t starts at t * stride elements (strides
+ *                 that are multiples of 8 and at least a row, so the three may
+ *                 be parts of one fused projection's rows); the heads of a
+ *                 token are contiguous
+ *   slot_mapping  [num_tokens] int32, as tv_kv_append; a token with a negative
+ *                 slot is padding and wholly skipped (its q_out row is left as
+ *                 it was); one with a slot beyond the pool is flagged
+ *                 TV_DEVERR_BAD_SLOT, its K and V are not written
+ *   positions     [num_axes][num_tokens] int32
+ *   pair_axis     [head_dim/2] int32, each in [0, num_axes)
+ * A token whose position on an axis that some pair uses is outside
+ * [0, rope_max_position) enters unrotated as a whole and flags
+ * TV_DEVERR_BAD_POSITION, and so does every token when pair_axis names no
+ * axis.  Two tokens mapped to one slot race, as in tv_kv_append.  q_out may
+ * be q itself (rows contiguous); it overlaps nothing else.
+ */
+tv_status tv_kv_append_mrope(void* q_out, const void* q, int64_t q_stride,
+                             const void* k_new, int64_t k_stride,
+                             const void* v_new, int64_t v_stride,
+                             const int32_t* slot_mapping,
+                             const int32_t* positions, int num_axes,
+                             const int32_t* pair_axis, int64_t num_tokens,
+                             void* k_pool, void* v_pool, int64_t num_pages,
+                             int num_q_heads, int num_kv_heads, int head_dim,
+                             int page_size, const float* rope_cos_sin,
+                             int rope_max_position, uint32_t* err,
+                             void* stream);
+
+/*
  * tv_paged_decode -- one query per sequence at position context_lens[s]-1
  * attends to keys 0 .. context_lens[s]-1 of its sequence, found through the
  * block table ([P1] "PagedAttention", "推理流程", "在线Softmax", "Llama 3.2
@@ -355,6 +394,72 @@ tv_status tv_prefill_workspace_size(int num_seqs, int max_query_len,
                                     size_t* bytes);
 
 /*
+ * tv_paged_chunk -- attention of a chunk of new rows per sequence over the
+ * paged cache, causal, from one row to long chunks in one call: draft tokens
+ * to verify, single decode tokens and prompt chunks.  The result is that of
+ * tv_paged_prefill (same rows, keys and layout: with T_s rows and C =
+ * context_lens[s], row i sees keys 0 .. C - T_s + i).  The source pages have
+ * one token per step or a prompt; this call serves what lies between, where a
+ * prefill tile would be mostly padding and one CTA would walk a long context
+ * alone.
+ *   out              [total_rows][num_q_heads][head_dim] bf16, written
+ *   q                [total_rows][num_q_heads][head_dim] bf16
+ *   num_query_rows   total_rows (the row count of q and out)
+ *   query_start_loc  [num_seqs + 1] int32, non-decreasing, [0] == 0,
+ *                    [num_seqs] <= num_query_rows; rows behind it are left
+ *                    as they were; a sequence may have no rows
+ *   max_query_len    >= every T_s
+ *   workspace        NULL (keys are not split), or device memory of at least
+ *                    tv_chunk_workspace_size() bytes, 16-byte aligned, no
+ *                    initial contents needed.  Calls that overlap on the GPU
+ *                    need separate workspaces.
+ *   workspace_bytes  its size; too small returns TV_ERR_INVALID_ARG
+ * A sequence with T_s > C, T_s > max_query_len or rows outside q is flagged
+ * TV_DEVERR_BAD_QUERY and skipped.  scale must be positive
+ * (TV_ERR_INVALID_ARG otherwise, as tv_paged_prefill); max_query_len times the
+ * group size is at most 2^20 - 16.  A key of a bad page is left out; a row
+ * that sees no key comes out zero.  What a key that a row does not see holds,
+ * NaN and infinities too, does not reach that row; an infinity or NaN in V
+ * that it sees makes that element of its output non-finite.
+ */
+tv_status tv_paged_chunk(void* out, const void* q, int64_t num_query_rows,
+                         const int32_t* query_start_loc, const void* k_pool,
+                         const void* v_pool, const int32_t* block_tables,
+                         int max_blocks_per_seq, const int32_t* context_lens,
+                         int num_seqs, int max_query_len, int num_q_heads,
+                         int num_kv_heads, int head_dim, int page_size,
+                         int64_t num_pages, float scale, void* workspace,
+                         size_t workspace_bytes, uint32_t* err,
+                         void* stream);
+
+/*
+ * tv_paged_cross_attention -- every query row of sequence s attends to all
+ * encoder_lens[s] states of its encoder, whose K and V are cached in pages
+ * once (tv_kv_append) and read through block_tables like any context; there
+ * is no mask, and T_s and encoder_lens[s] are independent (a sequence without
+ * states gets zero rows).  Arguments and behaviour otherwise as
+ * tv_paged_chunk.
+ */
+tv_status tv_paged_cross_attention(
+    void* out, const void* q, int64_t num_query_rows,
+    const int32_t* query_start_loc, const void* k_pool, const void* v_pool,
+    const int32_t* block_tables, int max_blocks_per_seq,
+    const int32_t* encoder_lens, int num_seqs, int max_query_len,
+    int num_q_heads, int num_kv_heads, int head_dim, int page_size,
+    int64_t num_pages, float scale, void* workspace, size_t workspace_bytes,
+    uint32_t* err, void* stream);
+
+/*
+ * tv_chunk_workspace_size -- bytes of the optional workspace of
+ * tv_paged_chunk and tv_paged_cross_attention on the current device for up to
+ * num_seqs sequences of up to max_query_len rows.
+ *   bytes   host pointer, written on TV_OK
+ */
+tv_status tv_chunk_workspace_size(int num_seqs, int max_query_len,
+                                  int num_q_heads, int num_kv_heads,
+                                  int head_dim, size_t* bytes);
+
+/*
  * tv_paged_decode_split_static -- tv_paged_decode_split followed by
  * tv_split_merge in one call that allocates nothing: the fp32 partials go to
  * a fixed array inside the library instead of caller buffers.  The source
@@ -504,6 +609,62 @@ tv_status tv_pool_release(int32_t* pool_state, int64_t num_pages,
                           int32_t* context_lens, int num_seqs,
                           const int32_t* seqs, int num_release, uint32_t* err,
                           void* stream);
+
+/*
+ * tv_pool_truncate -- every sequence keeps its first new_lens[s] tokens: the
+ * pages behind them lose this row's reference and their entries become -1,
+ * context_lens[s] = new_lens[s].  Pages whose count reaches zero go back on
+ * the stack in ascending id order, over all sequences of the call (rejected
+ * draft tokens, a return to an earlier point; new_lens[s] = 0 is a release).
+ *   new_lens   [num_seqs] int32; a negative length, or one above the context,
+ *              leaves that sequence as it is and flags TV_DEVERR_BAD_CONTEXT
+ */
+tv_status tv_pool_truncate(int32_t* pool_state, int64_t num_pages,
+                           int32_t* block_tables, int max_blocks_per_seq,
+                           int32_t* context_lens, const int32_t* new_lens,
+                           int num_seqs, uint32_t* err, void* stream);
+
+/*
+ * tv_pool_compact -- moves the pages in use to the front of the pool.  With U
+ * pages in use (count > 0), the i-th page in use with an id >= U moves to the
+ * i-th free page with an id < U (both in ascending order); counts and the
+ * entries of block_tables follow, and the free stack becomes that of
+ * tv_pool_init (pages U .. num_pages-1, U on top).  Afterwards pages U and up
+ * hold nothing, so the tail of the pool can serve other uses.
+ *   block_tables, context_lens   every row that holds pages of this pool
+ *   move_src, move_dst  device int32 arrays of max_moves >= num_pages / 2
+ *              entries: receive the moves, ascending in both
+ *   num_moves  device int32, receives their number; entries behind it are
+ *              left as they were
+ *   k_pool, v_pool  the pools of one layer, whose moved pages are copied, or
+ *              both NULL; tv_page_copy with the same lists moves the pages of
+ *              every further layer
+ * A page_size other than the state's flags TV_DEVERR_BAD_SEQ and changes
+ * nothing (*num_moves = 0).
+ */
+tv_status tv_pool_compact(int32_t* pool_state, int64_t num_pages,
+                          int32_t* block_tables, int max_blocks_per_seq,
+                          const int32_t* context_lens, int num_seqs,
+                          int32_t* move_src, int32_t* move_dst,
+                          int64_t max_moves, int32_t* num_moves, void* k_pool,
+                          void* v_pool, int num_kv_heads, int head_dim,
+                          int page_size, uint32_t* err, void* stream);
+
+/*
+ * tv_page_copy -- copies whole pages of K and of V inside the pools:
+ * page src_pages[i] to page dst_pages[i] for i < n, bit for bit.
+ *   src_pages, dst_pages  device int32 arrays of max_pairs entries
+ *   num_pairs  NULL (n = max_pairs), or a device int32 with n, clamped to
+ *              [0, max_pairs]
+ * A pair with an id outside the pool is skipped and flagged
+ * TV_DEVERR_BAD_PAGE.  The pairs are copied in no order: a page that is a
+ * destination twice, or a destination and the source of another pair, races.
+ */
+tv_status tv_page_copy(void* k_pool, void* v_pool, int64_t num_pages,
+                       const int32_t* src_pages, const int32_t* dst_pages,
+                       int64_t max_pairs, const int32_t* num_pairs,
+                       int num_kv_heads, int head_dim, int page_size,
+                       uint32_t* err, void* stream);
 
 /*
  * tv_decode_step -- one decode step of every live sequence, device-side

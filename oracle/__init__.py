@@ -131,6 +131,42 @@ def kv_append_rope(k_new, v_new, slot_mapping, positions, cos_sin, k_pool,
     return kp, vp, bad, bad_pos
 
 
+def mrope(rows, positions, pair_axis, cos_sin):
+    """Rotary positions on several axes: a rotated copy of the uint16 bf16 rows
+    [T][H][head_dim], pair i of token t by the angle cos_sin[p, :, i] of p =
+    positions[pair_axis[i], t].  Each token's angles are gathered into a row
+    of their own and the rows turned by ``rope`` at position t; a token with a
+    used position (or an axis) out of range stays as it is and is counted."""
+    pos = np.asarray(positions, np.int64)
+    axis = np.asarray(pair_axis, np.int64)
+    t = rows.shape[0]
+    ok = np.ones(t, bool)
+    table = np.zeros((max(t, 1), 2, axis.shape[0]), np.float32)
+    for i, a in enumerate(axis):
+        if not 0 <= a < pos.shape[0]:
+            ok[:] = False
+            continue
+        good = (pos[a] >= 0) & (pos[a] < cos_sin.shape[0])
+        ok &= good
+        table[:t][good, :, i] = cos_sin[pos[a][good], :, i]
+    return rope(rows, np.where(ok, np.arange(t), -1), table)
+
+
+def paged_cross(q, query_start_loc, k_pool, v_pool, block_tables,
+                encoder_lens, scale, allow_bad=False):
+    """Cross attention: every query row of sequence s over all encoder_lens[s]
+    cached states, i.e. a decode row of its own on that sequence's table:
+    float64 [rows][Hq][D] (rows behind the last sequence stay zero)."""
+    qsl = np.asarray(query_start_loc, np.int64)
+    seq = np.repeat(np.arange(len(qsl) - 1), np.diff(qsl))
+    out = np.zeros(q.shape, np.float64)
+    if len(seq):
+        out[:len(seq)] = paged_decode(
+            q[:len(seq)], k_pool, v_pool, np.asarray(block_tables)[seq],
+            np.asarray(encoder_lens)[seq], scale, allow_bad=allow_bad)
+    return out
+
+
 def paged_decode_rows(q, k_pool, v_pool, block_tables, context_lens, scale,
                       seq_idx, head_idx, with_lse=False, allow_bad=False):
     """Decode attention for selected (sequence, q-head) rows; float64 [n][D].

@@ -33,6 +33,13 @@ notes):
   * ``release``: every page reference of the listed sequences is dropped;
     pages whose count reaches zero return to the stack in ascending page id
     order; the rows become empty (context 0, entries -1).
+  * ``truncate``: a sequence keeps its first ``new_lens[s]`` tokens; its
+    references to the pages behind them are dropped, their entries become -1,
+    and over the whole call pages reaching zero return to the stack in
+    ascending id order.
+  * ``compact``: with U pages in use the i-th of them at or above U moves to
+    the i-th free page below U; tables and counts follow and the stack is
+    ``init``'s again.
   * ``fork``: the destination (empty) sequence takes the source's pages and
     context; every shared page's count grows by one.
 """
@@ -143,3 +150,38 @@ class PagePool:
             for b in range(n):
                 self.ref[int(block_tables[src][b])] += 1
             context_lens[dst] = context_lens[src]
+
+    def truncate(self, block_tables, context_lens, new_lens):
+        """Keep the first new_lens[s] tokens of every sequence."""
+        freed = set()
+        for s, n in enumerate(new_lens):
+            if not 0 <= n <= context_lens[s]:
+                continue
+            for b in range(pages_for(n, self.ps),
+                           pages_for(context_lens[s], self.ps)):
+                p = int(block_tables[s][b])
+                self.ref[p] -= 1
+                if self.ref[p] == 0:
+                    freed.add(p)
+                block_tables[s][b] = -1
+            context_lens[s] = n
+        for p in sorted(freed):
+            self.stack.append(p)
+
+    def compact(self, block_tables, context_lens, k_pool=None, v_pool=None):
+        """Move the pages in use to the front; returns the (src, dst) moves."""
+        used = int((self.ref > 0).sum())
+        src = [p for p in range(used, self.num_pages) if self.ref[p] > 0]
+        dst = [p for p in range(used) if self.ref[p] == 0]
+        new = dict(zip(src, dst))
+        for s, ctx in enumerate(context_lens):
+            for b in range(pages_for(ctx, self.ps)):
+                p = int(block_tables[s][b])
+                block_tables[s][b] = new.get(p, p)
+        for a, b in new.items():
+            self.ref[b], self.ref[a] = self.ref[a], 0
+            if k_pool is not None:
+                k_pool[b] = k_pool[a]
+                v_pool[b] = v_pool[a]
+        self.stack = list(range(self.num_pages - 1, used - 1, -1))
+        return list(new.items())

@@ -69,6 +69,22 @@ SIGNATURES = {
                                   _I, _I, _I, _P, _P]),
     "tv_pool_fork": (_I, [_P, _I64, _P, _I, _P, _I, _P, _P, _I, _P, _P]),
     "tv_pool_release": (_I, [_P, _I64, _P, _I, _P, _I, _P, _I, _P, _P]),
+    "tv_kv_append_mrope": (_I, [_P, _P, _I64, _P, _I64, _P, _I64, _P, _P, _I,
+                                _P, _I64, _P, _P, _I64, _I, _I, _I, _I, _P,
+                                _I, _P, _P]),
+    "tv_paged_chunk": (_I, [_P, _P, _I64, _P, _P, _P, _P, _I, _P, _I, _I, _I,
+                            _I, _I, _I, _I64, _F, _P, ctypes.c_size_t, _P,
+                            _P]),
+    "tv_paged_cross_attention": (_I, [_P, _P, _I64, _P, _P, _P, _P, _I, _P,
+                                      _I, _I, _I, _I, _I, _I, _I64, _F, _P,
+                                      ctypes.c_size_t, _P, _P]),
+    "tv_chunk_workspace_size": (_I, [_I, _I, _I, _I, _I,
+                                     ctypes.POINTER(ctypes.c_size_t)]),
+    "tv_pool_truncate": (_I, [_P, _I64, _P, _I, _P, _P, _I, _P, _P]),
+    "tv_pool_compact": (_I, [_P, _I64, _P, _I, _P, _I, _P, _P, _I64, _P, _P,
+                             _P, _I, _I, _I, _P, _P]),
+    "tv_page_copy": (_I, [_P, _P, _I64, _P, _P, _I64, _P, _I, _I, _I, _P,
+                          _P]),
     "tv_decode_step": (_I, [_P, _I64, _P, _P, _P, _P, _P, _P, _P, _I, _P, _I,
                             _I, _I, _I, _I, _F, _P, ctypes.c_size_t, _P,
                             _P]),
@@ -132,6 +148,21 @@ def _stream(stream):
     return ctypes.c_void_p(stream.cuda_stream)
 
 
+def _launch(stream, *tensors):
+    """The device guard and stream pointer of a call on ``tensors`` (None
+    entries skipped): all of them on one device, the stream on it too."""
+    tensors = [t for t in tensors if t is not None]
+    dev = tensors[0].device
+    for t in tensors:
+        if t.device != dev:
+            raise ValueError(f"tensors on {dev} and {t.device} in one call")
+    if stream is None:
+        stream = torch.cuda.current_stream(dev)
+    elif stream.device != dev:
+        raise ValueError(f"stream on {stream.device}, tensors on {dev}")
+    return torch.cuda.device(dev), ctypes.c_void_p(stream.cuda_stream)
+
+
 def tv_kv_append(k_new, v_new, slot_mapping, k_pool, v_pool, err=None,
                  stream=None):
     """Scatter k_new/v_new [T][Hkv][D] (bf16) into pool slots
@@ -186,6 +217,70 @@ def tv_kv_append_rope(k_new, v_new, slot_mapping, positions, k_pool, v_pool,
         k_new.shape[0], _ptr(k_pool), _ptr(v_pool), num_pages, hkv, d,
         page_size, _ptr(cos_sin), max_pos, _ptr(err), _stream(stream)),
         "tv_kv_append_rope")
+
+
+def _token_rows(t, name):
+    """Row stride of t [T][H][D] (bf16, CUDA), whose heads are contiguous;
+    token rows may be strided (a part of a fused projection)."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be on a CUDA device")
+    if t.dtype != torch.bfloat16:
+        raise TypeError(f"{name} must be {torch.bfloat16}, got {t.dtype}")
+    if t.dim() != 3 or (t.numel() and (
+            t.stride(2) != 1 or (t.shape[1] > 1
+                                 and t.stride(1) != t.shape[2]))):
+        raise ValueError(f"{name} must be [T][H][D] with contiguous heads")
+    row = t.shape[1] * t.shape[2]
+    return t.stride(0) if t.shape[0] > 1 else row
+
+
+def tv_kv_append_mrope(q_out, q, k_new, v_new, slot_mapping, positions,
+                       pair_axis, k_pool, v_pool, cos_sin, err=None,
+                       stream=None):
+    """Append of tokens with a position on each of several axes: pair i of
+    every q and K head turns by the angle of positions[pair_axis[i]] (RoPE
+    table as tv_kv_append_rope), q into q_out [T][Hq][D], K and V into their
+    slots.  q, k_new, v_new [T][H][D] may have strided token rows; positions
+    is [axes][T], pair_axis [D/2] int32.  q and q_out None: K and V only."""
+    lib = load()
+    if (q is None) != (q_out is None):
+        raise ValueError("q and q_out go together")
+    ks, vs = _token_rows(k_new, "k_new"), _token_rows(v_new, "v_new")
+    bf, i32 = torch.bfloat16, torch.int32
+    _cuda(k_pool, bf, "k_pool"), _cuda(v_pool, bf, "v_pool")
+    _cuda(slot_mapping, i32, "slot_mapping"), _cuda(positions, i32,
+                                                    "positions")
+    _cuda(pair_axis, i32, "pair_axis")
+    if err is not None:
+        _cuda(err, i32, "err")
+    num_pages, page_size, hkv, d = k_pool.shape
+    t = k_new.shape[0]
+    if v_pool.shape != k_pool.shape or k_new.shape != v_new.shape:
+        raise ValueError("K/V shape mismatch")
+    if k_new.shape[1:] != (hkv, d) or slot_mapping.shape != (t,) or \
+            positions.dim() != 2 or positions.shape[1] != t or \
+            pair_axis.shape != (d // 2,):
+        raise ValueError("k_new must be [T][Hkv][D] with slot_mapping [T], "
+                         "positions [axes][T] and pair_axis [D/2]")
+    qs, hq = 0, 0
+    if q is not None:
+        qs = _token_rows(q, "q")
+        _cuda(q_out, bf, "q_out")
+        hq = q.shape[1]
+        if q.shape != (t, hq, d) or q_out.shape != q.shape:
+            raise ValueError("q and q_out must be [T][Hq][D]")
+    max_pos = _rope_table(cos_sin, d)
+    guard, st = _launch(stream, k_pool, v_pool, k_new, v_new, q, q_out,
+                        slot_mapping, positions, pair_axis, cos_sin, err)
+    with guard:
+        _check(lib.tv_kv_append_mrope(
+            _ptr(q_out), _ptr(q), qs, _ptr(k_new), ks, _ptr(v_new), vs,
+            _ptr(slot_mapping), _ptr(positions), positions.shape[0],
+            _ptr(pair_axis), t, _ptr(k_pool), _ptr(v_pool), num_pages, hq,
+            hkv, d, page_size, _ptr(cos_sin), max_pos, _ptr(err), st),
+            "tv_kv_append_mrope")
 
 
 def tv_paged_decode_append_rope(out, q, k_new, v_new, k_pool, v_pool,
@@ -360,6 +455,84 @@ def tv_paged_prefill(out, q, query_start_loc, k_pool, v_pool, block_tables,
         _ptr(context_lens), b, int(max_query_len), hq, hkv, d, page_size,
         num_pages, float(scale), _ptr(ws), ws_bytes, _ptr(err),
         _stream(stream)), "tv_paged_prefill")
+
+
+def tv_chunk_workspace_size(num_seqs, max_query_len, num_q_heads,
+                            num_kv_heads, head_dim=64):
+    """Bytes of workspace tv_paged_chunk and tv_paged_cross_attention use on
+    the current device."""
+    n = ctypes.c_size_t(0)
+    _check(load().tv_chunk_workspace_size(
+        int(num_seqs), int(max_query_len), int(num_q_heads),
+        int(num_kv_heads), int(head_dim), ctypes.byref(n)),
+        "tv_chunk_workspace_size")
+    return n.value
+
+
+def chunk_workspace(num_seqs, max_query_len, num_q_heads, num_kv_heads,
+                    device=None):
+    """Workspace of tv_paged_chunk / tv_paged_cross_attention (no initial
+    contents needed)."""
+    device = torch.device(device or "cuda")
+    with torch.cuda.device(device):
+        n = tv_chunk_workspace_size(num_seqs, max_query_len, num_q_heads,
+                                    num_kv_heads)
+        return torch.empty(max(n, 16), dtype=torch.uint8, device=device)
+
+
+def _chunk(name, out, q, query_start_loc, k_pool, v_pool, block_tables, lens,
+           lens_name, scale, max_query_len, workspace, err, stream):
+    lib = load()
+    bf = torch.bfloat16
+    for n, t in (("out", out), ("q", q), ("k_pool", k_pool),
+                 ("v_pool", v_pool)):
+        _cuda(t, bf, n)
+    for n, t in (("query_start_loc", query_start_loc),
+                 ("block_tables", block_tables), (lens_name, lens)):
+        _cuda(t, torch.int32, n)
+    if err is not None:
+        _cuda(err, torch.int32, "err")
+    if workspace is not None:
+        _cuda(workspace, torch.uint8, "workspace")
+    num_pages, page_size, hkv, d = k_pool.shape
+    rows, hq, qd = q.shape
+    b = lens.shape[0]
+    if out.shape != q.shape or qd != d or v_pool.shape != k_pool.shape or \
+            lens.dim() != 1 or query_start_loc.shape != (b + 1,) or \
+            block_tables.dim() != 2 or block_tables.shape[0] != b:
+        raise ValueError("shape mismatch")
+    guard, st = _launch(stream, q, out, query_start_loc, k_pool, v_pool,
+                        block_tables, lens, workspace, err)
+    with guard:
+        _check(getattr(lib, name)(
+            _ptr(out), _ptr(q), rows, _ptr(query_start_loc), _ptr(k_pool),
+            _ptr(v_pool), _ptr(block_tables), block_tables.shape[1],
+            _ptr(lens), b, int(max_query_len), hq, hkv, d, page_size,
+            num_pages, float(scale), _ptr(workspace),
+            workspace.numel() if workspace is not None else 0, _ptr(err), st),
+            name)
+
+
+def tv_paged_chunk(out, q, query_start_loc, k_pool, v_pool, block_tables,
+                   context_lens, scale, max_query_len, workspace=None,
+                   err=None, stream=None):
+    """out[rows][Hq][D] (bf16) = causal attention of a chunk of new rows per
+    sequence (one row to long chunks in one call) over the paged cache; with
+    a ``workspace`` (chunk_workspace) long contexts are split over keys."""
+    _chunk("tv_paged_chunk", out, q, query_start_loc, k_pool, v_pool,
+           block_tables, context_lens, "context_lens", scale, max_query_len,
+           workspace, err, stream)
+
+
+def tv_paged_cross_attention(out, q, query_start_loc, k_pool, v_pool,
+                             block_tables, encoder_lens, scale,
+                             max_query_len, workspace=None, err=None,
+                             stream=None):
+    """out[rows][Hq][D] (bf16) = attention of every query row of sequence s to
+    all encoder_lens[s] cached encoder states (no mask)."""
+    _chunk("tv_paged_cross_attention", out, q, query_start_loc, k_pool,
+           v_pool, block_tables, encoder_lens, "encoder_lens", scale,
+           max_query_len, workspace, err, stream)
 
 
 def tv_paged_decode_split_static(out, q, k_pool, v_pool, block_tables,
@@ -540,6 +713,96 @@ def tv_pool_release(state, block_tables, context_lens, seqs, err=None,
     _check(lib.tv_pool_release(_ptr(state), num_pages, _ptr(block_tables), mb,
                                _ptr(context_lens), b, _ptr(seqs), seqs.numel(),
                                _ptr(err), _stream(stream)), "tv_pool_release")
+
+
+def tv_pool_truncate(state, block_tables, context_lens, new_lens, err=None,
+                     stream=None):
+    """Every sequence keeps its first new_lens[s] tokens; pages behind them
+    that nobody else holds go back to the pool."""
+    lib = load()
+    num_pages = _pool_pages(state)
+    mb, b = _pool_tables(block_tables, context_lens)
+    _cuda(new_lens, torch.int32, "new_lens")
+    if new_lens.shape != context_lens.shape:
+        raise ValueError("new_lens and context_lens differ in length")
+    if err is not None:
+        _cuda(err, torch.int32, "err")
+    guard, st = _launch(stream, state, block_tables, context_lens, new_lens,
+                        err)
+    with guard:
+        _check(lib.tv_pool_truncate(
+            _ptr(state), num_pages, _ptr(block_tables), mb,
+            _ptr(context_lens), _ptr(new_lens), b, _ptr(err), st),
+            "tv_pool_truncate")
+
+
+def pool_moves(num_pages, device=None):
+    """Move lists [2][num_pages // 2] and their count for tv_pool_compact."""
+    device = device or "cuda"
+    return (torch.zeros(2, max(1, num_pages // 2), dtype=torch.int32,
+                        device=device),
+            torch.zeros(1, dtype=torch.int32, device=device))
+
+
+def tv_pool_compact(state, block_tables, context_lens, moves, num_moves,
+                    k_pool=None, v_pool=None, page_size=None, err=None,
+                    stream=None):
+    """Pages in use move to the front of the pool; moves[0][:n] -> moves[1][:n]
+    with n = num_moves (see pool_moves) lists them for tv_page_copy on further
+    layers' pools.  page_size is the pools' when they are given."""
+    lib = load()
+    num_pages = _pool_pages(state)
+    mb, b = _pool_tables(block_tables, context_lens)
+    _cuda(moves, torch.int32, "moves"), _cuda(num_moves, torch.int32,
+                                              "num_moves")
+    if moves.dim() != 2 or moves.shape[0] != 2 or num_moves.numel() < 1:
+        raise ValueError("moves must be [2][max_moves], num_moves [1]")
+    if (k_pool is None) != (v_pool is None):
+        raise ValueError("k_pool and v_pool go together")
+    ps, hkv, d = page_size or 16, 1, 64
+    if k_pool is not None:
+        _cuda(k_pool, torch.bfloat16, "k_pool")
+        _cuda(v_pool, torch.bfloat16, "v_pool")
+        if k_pool.shape[0] != num_pages or v_pool.shape != k_pool.shape:
+            raise ValueError("pool_state and the pools disagree on num_pages")
+        if page_size not in (None, k_pool.shape[1]):
+            raise ValueError("page_size is not the pools'")
+        _, ps, hkv, d = k_pool.shape
+    if err is not None:
+        _cuda(err, torch.int32, "err")
+    guard, st = _launch(stream, state, block_tables, context_lens, moves,
+                        num_moves, k_pool, v_pool, err)
+    with guard:
+        _check(lib.tv_pool_compact(
+            _ptr(state), num_pages, _ptr(block_tables), mb,
+            _ptr(context_lens), b, _ptr(moves[0]), _ptr(moves[1]),
+            moves.shape[1], _ptr(num_moves), _ptr(k_pool), _ptr(v_pool), hkv,
+            d, ps, _ptr(err), st), "tv_pool_compact")
+
+
+def tv_page_copy(k_pool, v_pool, src_pages, dst_pages, num_pairs=None,
+                 err=None, stream=None):
+    """Copy whole pages src_pages[i] -> dst_pages[i] of both pools, all of
+    them or the first num_pairs (a device int32)."""
+    lib = load()
+    _cuda(k_pool, torch.bfloat16, "k_pool"), _cuda(v_pool, torch.bfloat16,
+                                                   "v_pool")
+    _cuda(src_pages, torch.int32, "src_pages")
+    _cuda(dst_pages, torch.int32, "dst_pages")
+    for n, t in (("num_pairs", num_pairs), ("err", err)):
+        if t is not None:
+            _cuda(t, torch.int32, n)
+    if v_pool.shape != k_pool.shape or src_pages.dim() != 1 or \
+            src_pages.shape != dst_pages.shape:
+        raise ValueError("shape mismatch")
+    num_pages, ps, hkv, d = k_pool.shape
+    guard, st = _launch(stream, k_pool, v_pool, src_pages, dst_pages,
+                        num_pairs, err)
+    with guard:
+        _check(lib.tv_page_copy(
+            _ptr(k_pool), _ptr(v_pool), num_pages, _ptr(src_pages),
+            _ptr(dst_pages), src_pages.numel(), _ptr(num_pairs), hkv, d, ps,
+            _ptr(err), st), "tv_page_copy")
 
 
 def tv_decode_step(state, out, q, k_new, v_new, k_pool, v_pool, block_tables,

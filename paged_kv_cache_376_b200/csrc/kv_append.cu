@@ -93,7 +93,94 @@ __global__ void __launch_bounds__(256)
   }
 }
 
+// RoPE by positions of several axes, on q and K.  Pair (i, i + 32) of every
+// head turns by the angle of positions[pair_axis[i]] (time, height, width, ...
+// of an image or video token), looked up in one cos/sin table; the arithmetic
+// is that of kv_append_rope_kernel.
+//
+// Bound: bytes, 2 x (Hq + 2 Hkv) x 128 per token plus its angles.  One warp per
+// token: lane i looks up pair i's angle once (its axis, its position, two table
+// entries), the lanes exchange them by shuffles, and every lane turns the
+// vector pair u = lane & 3 (dimensions 8u .. 8u + 7 with + 32) of heads
+// lane >> 2, + 8, + 16, ... , so the angles are read once per token however
+// many heads it has.
+template <int kHeads>   // heads of a lane in flight at once
+__global__ void __launch_bounds__(256)
+    kv_append_mrope_kernel(const MropeArgs a) {
+  const int lane = threadIdx.x & 31;
+  const int u = lane & 3;
+  const int heads = a.num_q_heads + 2 * a.num_kv_heads;
+  const int axis = a.pair_axis[lane];
+  const bool axis_ok = axis >= 0 && axis < a.num_axes;
+  const int64_t stride = (int64_t)gridDim.x * (blockDim.x >> 5);
+  for (int64_t t = blockIdx.x * (int64_t)(blockDim.x >> 5) + (threadIdx.x >> 5);
+       t < a.num_tokens; t += stride) {
+    const int64_t slot = a.slot_mapping[t];
+    const int pos = axis_ok ? a.positions[axis * a.num_tokens + t] : -1;
+    if (slot < 0) continue;                  // padding
+    const bool slot_ok = slot < a.num_slots;
+    // a token turns as a whole or, with a bad position, not at all
+    const bool turn = __all_sync(0xffffffffu, pos >= 0 && pos < a.max_position);
+    if (lane == 0) {
+      if (!slot_ok) flag_error(a.err, DEVERR_BAD_SLOT);
+      if (!turn) flag_error(a.err, DEVERR_BAD_POSITION);
+    }
+    float cl = 1.f, sl = 0.f;
+    if (turn) {
+      cl = __ldg(a.cos_sin + (size_t)pos * 64 + lane);
+      sl = __ldg(a.cos_sin + (size_t)pos * 64 + 32 + lane);
+    }
+    float c8[8], s8[8];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      c8[k] = __shfl_sync(0xffffffffu, cl, 8 * u + k);
+      s8[k] = __shfl_sync(0xffffffffu, sl, 8 * u + k);
+    }
+    for (int h0 = lane >> 2; h0 < heads; h0 += 8 * kHeads) {
+      uint4 lo[kHeads], hi[kHeads];
+#pragma unroll
+      for (int n = 0; n < kHeads; ++n) {
+        const int h = h0 + 8 * n;
+        if (h >= heads) continue;
+        const int hk = h - a.num_q_heads, hv = hk - a.num_kv_heads;
+        const __nv_bfloat16* src =
+            hk < 0   ? a.q + t * a.q_stride + h * 64
+            : hv < 0 ? a.k_new + t * a.k_stride + hk * 64
+                     : a.v_new + t * a.v_stride + hv * 64;
+        lo[n] = reinterpret_cast<const uint4*>(src)[u];
+        hi[n] = reinterpret_cast<const uint4*>(src)[u + 4];
+      }
+#pragma unroll
+      for (int n = 0; n < kHeads; ++n) {
+        const int h = h0 + 8 * n;
+        if (h >= heads) continue;
+        const int hk = h - a.num_q_heads, hv = hk - a.num_kv_heads;
+        if (hk >= 0 && !slot_ok) continue;
+        if (hv < 0 && turn) rope_rotate8(lo[n], hi[n], c8, s8);
+        __nv_bfloat16* dst =
+            hk < 0   ? a.q_out + (t * a.num_q_heads + h) * 64
+            : hv < 0 ? a.k_pool + (slot * a.num_kv_heads + hk) * 64
+                     : a.v_pool + (slot * a.num_kv_heads + hv) * 64;
+        reinterpret_cast<uint4*>(dst)[u] = lo[n];
+        reinterpret_cast<uint4*>(dst)[u + 4] = hi[n];
+      }
+    }
+  }
+}
+
 }  // namespace
+
+cudaError_t launch_kv_append_mrope(const MropeArgs& a, cudaStream_t stream) {
+  if (a.num_tokens == 0) return cudaSuccess;
+  int dev = 0, sms = 148;
+  cudaGetDevice(&dev);
+  cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  const int64_t want = (a.num_tokens + 7) / 8;
+  const int64_t cap = (int64_t)sms * 8;
+  kv_append_mrope_kernel<3>
+      <<<(int)(want < cap ? want : cap), 256, 0, stream>>>(a);
+  return cudaGetLastError();
+}
 
 cudaError_t launch_kv_append_rope(const void* k_new, const void* v_new,
                                   const int32_t* slot_mapping,

@@ -392,7 +392,257 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (threadIdx.x == 0) *p.top = min(top + base, p.num_pages);
 }
 
+// ---- truncate -----------------------------------------------------------------
+// Sequence s keeps its first new_lens[s] tokens: the pages behind them lose a
+// reference, and those that nobody holds any more go back on the stack in
+// ascending id order, as in a release.
+//
+// Bound: latency (a few integers per dropped page).  One warp per sequence, a
+// lane per dropped page; the freed pages are marked in a bitmap (one bit per
+// page, in the scratch words), whose order is the id order, so a scan over
+// num_pages / 32 words replaces a sort.
+__global__ void __launch_bounds__(kThreads, 1)
+    pool_truncate_kernel(PoolView p, int32_t* bt, int mb, int32_t* ctx,
+                         const int32_t* new_lens, int num_seqs,
+                         uint32_t* err) {
+  __shared__ int sh[33];
+  const int kPS = *p.page_size;
+  const int lane = threadIdx.x & 31;
+  uint32_t* marks = reinterpret_cast<uint32_t*>(p.cnt_app);
+  for (int s = threadIdx.x >> 5; s < num_seqs; s += kThreads / 32) {
+    const int c = ctx[s], n = new_lens[s];
+    if (c < 0 || c > mb * kPS || n < 0 || n > c) {
+      if (lane == 0) flag_error(err, DEVERR_BAD_CONTEXT);
+      continue;
+    }
+    const int last = pages_for(c, kPS);
+    for (int k = pages_for(n, kPS) + lane; k < last; k += 32) {
+      const int page = bt[(size_t)s * mb + k];
+      bt[(size_t)s * mb + k] = -1;
+      if (page < 0 || page >= p.num_pages)
+        flag_error(err, DEVERR_BAD_PAGE);
+      else if (atomicSub(p.ref + page, 1) == 1)
+        atomicOr(marks + (page >> 5), 1u << (page & 31));
+    }
+    __syncwarp();
+    if (lane == 0) ctx[s] = n;
+  }
+  __syncthreads();
+  const int words = (p.num_pages + 31) / 32;
+  int top = *p.top;
+  for (int w0 = 0; w0 < words; w0 += kThreads) {
+    const int w = w0 + threadIdx.x;
+    uint32_t bits = w < words ? __ldcg(marks + w) : 0u;
+    int tot;
+    int pos = top + block_exclusive_scan(__popc(bits), sh, &tot);
+    if (bits) marks[w] = 0;
+    for (; bits; bits &= bits - 1, ++pos) {
+      // a consistent pool never overflows; a corrupted one is flagged
+      if (pos < p.num_pages)
+        p.stack[pos] = 32 * w + __ffs(bits) - 1;
+      else
+        flag_error(err, DEVERR_BAD_SEQ);
+    }
+    top += tot;
+  }
+  __syncthreads();
+  if (threadIdx.x == 0) *p.top = min(top, p.num_pages);
+}
+
+// ---- compaction -----------------------------------------------------------------
+// With U pages in use (count > 0), the i-th used page at or above U moves to
+// the i-th free page below U; both lists are ascending and equally long.  Then
+// the pages in use are exactly 0 .. U - 1 and the free stack is rebuilt as init
+// leaves it.  This kernel (one CTA) plans: counts as bit words, their scan, the
+// move lists, the counts and the stack.
+__global__ void __launch_bounds__(kThreads, 1)
+    pool_compact_plan_kernel(PoolView p, int page_size, int32_t* move_src,
+                             int32_t* move_dst, int32_t* num_moves,
+                             uint32_t* err) {
+  __shared__ int sh[33];
+  const int n = p.num_pages;
+  const int words = (n + 31) / 32;
+  if (*p.page_size != page_size) {   // pools of another page size
+    if (threadIdx.x == 0) {
+      flag_error(err, DEVERR_BAD_SEQ);
+      *num_moves = 0;
+    }
+    return;
+  }
+  uint32_t* held = reinterpret_cast<uint32_t*>(p.cnt_app);
+  int mine = 0;
+  for (int i = threadIdx.x; i < 32 * words; i += kThreads) {
+    const uint32_t b =
+        __ballot_sync(0xffffffffu, i < n && p.ref[i] > 0);
+    if ((threadIdx.x & 31) == 0) {
+      held[i >> 5] = b;
+      mine += __popc(b);
+    }
+  }
+  int used;
+  (void)block_exclusive_scan(mine, sh, &used);   // its barriers order `held`
+  int ns = 0, nd = 0;
+  for (int w0 = 0; w0 < words; w0 += kThreads) {
+    const int w = w0 + threadIdx.x;
+    uint32_t src = 0, dst = 0;
+    if (w < words) {
+      const uint32_t b = held[w];
+      held[w] = 0;
+      // bits of this word whose page id is below `used`
+      const int k = used - 32 * w;
+      const uint32_t low = k >= 32 ? 0xffffffffu : k <= 0 ? 0u : (1u << k) - 1;
+      src = b & ~low;
+      dst = ~b & low;
+    }
+    int ts, td;
+    int ps = ns + block_exclusive_scan(__popc(src), sh, &ts);
+    int pd = nd + block_exclusive_scan(__popc(dst), sh, &td);
+    for (; src; src &= src - 1) move_src[ps++] = 32 * w + __ffs(src) - 1;
+    for (; dst; dst &= dst - 1) move_dst[pd++] = 32 * w + __ffs(dst) - 1;
+    ns += ts;
+    nd += td;
+  }
+  __syncthreads();
+  for (int i = threadIdx.x; i < ns; i += kThreads) {
+    const int a = move_src[i], b = move_dst[i];
+    p.ref[b] = p.ref[a];
+    p.ref[a] = 0;
+  }
+  for (int i = threadIdx.x; i < n - used; i += kThreads)
+    p.stack[i] = n - 1 - i;
+  if (threadIdx.x == 0) {
+    *p.top = n - used;
+    *num_moves = ns;
+  }
+}
+
+// Block-table entries follow their pages: a binary search in the ascending
+// list of moved pages (entries below its first page did not move).
+__global__ void __launch_bounds__(256)
+    pool_compact_tables_kernel(int32_t* bt, int mb, const int32_t* ctx,
+                               int num_seqs, int kPS, const int32_t* move_src,
+                               const int32_t* move_dst,
+                               const int32_t* num_moves, uint32_t* err) {
+  const int n = *num_moves;
+  const int first = n > 0 ? move_src[0] : 0;
+  const int64_t total = (int64_t)num_seqs * mb;
+  for (int64_t i = blockIdx.x * (int64_t)blockDim.x + threadIdx.x; i < total;
+       i += (int64_t)gridDim.x * blockDim.x) {
+    const int s = (int)(i / mb), b = (int)(i % mb);
+    int c = ctx[s];
+    if (c < 0 || c > mb * kPS) {
+      if (b == 0) flag_error(err, DEVERR_BAD_CONTEXT);
+      c = c < 0 ? 0 : mb * kPS;
+    }
+    if (n == 0 || b >= pages_for(c, kPS)) continue;
+    const int page = bt[i];
+    if (page < first) continue;
+    int lo = 0, hi = n;             // first entry >= page
+    while (lo < hi) {
+      const int mid = (lo + hi) >> 1;
+      if (__ldg(move_src + mid) < page) lo = mid + 1;
+      else hi = mid;
+    }
+    if (lo < n && move_src[lo] == page) bt[i] = move_dst[lo];
+  }
+}
+
+// Whole pages of K and V, src[i] to dst[i]: HBM-bound (2 x the bytes moved).
+// A unit is 16 KB of one tensor: 256 threads x four 16-byte vectors in flight.
+__global__ void __launch_bounds__(256)
+    page_copy_kernel(uint4* k_pool, uint4* v_pool, int num_pages,
+                     int page_vecs, const int32_t* src, const int32_t* dst,
+                     int64_t max_pairs, const int32_t* num_pairs,
+                     uint32_t* err) {
+  constexpr int kUnit = 1024;
+  int64_t n = max_pairs;
+  if (num_pairs) {
+    n = *num_pairs;
+    n = n < 0 ? 0 : (n > max_pairs ? max_pairs : n);
+  }
+  const int per = (page_vecs + kUnit - 1) / kUnit;   // units of a page
+  for (int64_t i = blockIdx.x; i < n * 2 * per; i += gridDim.x) {
+    const int64_t pair = i / (2 * per);
+    const int r = (int)(i - pair * 2 * per);
+    const int a = src[pair], b = dst[pair];
+    if (a < 0 || a >= num_pages || b < 0 || b >= num_pages) {
+      if (threadIdx.x == 0 && r == 0) flag_error(err, DEVERR_BAD_PAGE);
+      continue;
+    }
+    uint4* pool = r < per ? k_pool : v_pool;
+    const int v0 = (r < per ? r : r - per) * kUnit;
+    const uint4* from = pool + (size_t)a * page_vecs + v0;
+    uint4* to = pool + (size_t)b * page_vecs + v0;
+    uint4 x[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const int v = threadIdx.x + 256 * k;
+      if (v0 + v < page_vecs) x[k] = from[v];
+    }
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const int v = threadIdx.x + 256 * k;
+      if (v0 + v < page_vecs) to[v] = x[k];
+    }
+  }
+}
+
 }  // namespace
+
+cudaError_t launch_pool_truncate(int32_t* state, int num_pages, int32_t* bt,
+                                 int mb, int32_t* ctx, const int32_t* new_lens,
+                                 int num_seqs, uint32_t* err,
+                                 cudaStream_t stream) {
+  pool_truncate_kernel<<<1, kThreads, 0, stream>>>(
+      view(state, num_pages), bt, mb, ctx, new_lens, num_seqs, err);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_pool_compact(int32_t* state, int num_pages, int page_size,
+                                int32_t* bt, int mb, const int32_t* ctx,
+                                int num_seqs, int32_t* move_src,
+                                int32_t* move_dst, int32_t* num_moves,
+                                void* k_pool, void* v_pool, int row_bytes,
+                                uint32_t* err, cudaStream_t stream) {
+  pool_compact_plan_kernel<<<1, kThreads, 0, stream>>>(
+      view(state, num_pages), page_size, move_src, move_dst, num_moves, err);
+  cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  int dev = 0, sms = 148;
+  cudaGetDevice(&dev);
+  cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  const int64_t want = ((int64_t)num_seqs * mb + 255) / 256;
+  const int64_t cap = (int64_t)sms * 8;
+  if (num_seqs > 0) {
+    pool_compact_tables_kernel<<<(int)(want < cap ? want : cap), 256, 0,
+                                 stream>>>(bt, mb, ctx, num_seqs, page_size,
+                                           move_src, move_dst, num_moves, err);
+    e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+  }
+  if (!k_pool) return cudaSuccess;
+  return launch_page_copy(k_pool, v_pool, num_pages, page_size * row_bytes,
+                          move_src, move_dst, num_pages / 2, num_moves, err,
+                          stream);
+}
+
+cudaError_t launch_page_copy(void* k_pool, void* v_pool, int num_pages,
+                             int page_bytes, const int32_t* src,
+                             const int32_t* dst, int64_t max_pairs,
+                             const int32_t* num_pairs, uint32_t* err,
+                             cudaStream_t stream) {
+  if (max_pairs == 0) return cudaSuccess;
+  int dev = 0, sms = 148;
+  cudaGetDevice(&dev);
+  cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  const int page_vecs = page_bytes / 16;
+  const int64_t want = max_pairs * 2 * ((page_vecs + 1023) / 1024);
+  const int64_t cap = (int64_t)sms * 8;
+  page_copy_kernel<<<(int)(want < cap ? want : cap), 256, 0, stream>>>(
+      static_cast<uint4*>(k_pool), static_cast<uint4*>(v_pool), num_pages,
+      page_vecs, src, dst, max_pairs, num_pairs, err);
+  return cudaGetLastError();
+}
 
 cudaError_t launch_pool_init(int32_t* state, int num_pages, int page_size,
                              const int32_t* bt, int mb, const int32_t* ctx,

@@ -187,6 +187,61 @@ tv_status tv_kv_append_rope(const void* k_new, const void* v_new,
       err, static_cast<cudaStream_t>(stream)));
 }
 
+tv_status tv_kv_append_mrope(void* q_out, const void* q, int64_t q_stride,
+                             const void* k_new, int64_t k_stride,
+                             const void* v_new, int64_t v_stride,
+                             const int32_t* slot_mapping,
+                             const int32_t* positions, int num_axes,
+                             const int32_t* pair_axis, int64_t num_tokens,
+                             void* k_pool, void* v_pool, int64_t num_pages,
+                             int num_q_heads, int num_kv_heads, int head_dim,
+                             int page_size, const float* rope_cos_sin,
+                             int rope_max_position, uint32_t* err,
+                             void* stream) {
+  if (num_tokens < 0 || num_pages <= 0 || num_kv_heads <= 0 || num_axes <= 0 ||
+      (q_out != nullptr) != (q != nullptr) || (q && num_q_heads <= 0))
+    return TV_ERR_INVALID_ARG;
+  if (head_dim != kHeadDim || !page_size_ok(page_size))
+    return TV_ERR_UNSUPPORTED;
+  if (num_tokens == 0) return TV_OK;
+  if (!k_new || !v_new || !slot_mapping || !positions || !pair_axis ||
+      !k_pool || !v_pool || !rope_cos_sin || rope_max_position <= 0)
+    return TV_ERR_INVALID_ARG;
+  if (!aligned16(q) || !aligned16(q_out) || !aligned16(k_new) ||
+      !aligned16(v_new) || !aligned16(k_pool) || !aligned16(v_pool) ||
+      !aligned16(rope_cos_sin))
+    return TV_ERR_INVALID_ARG;
+  // token rows start on 16-byte boundaries and do not overlap
+  const int64_t q_row = (int64_t)num_q_heads * head_dim;
+  const int64_t kv_row = (int64_t)num_kv_heads * head_dim;
+  if ((q && (q_stride < q_row || q_stride % 8)) || k_stride < kv_row ||
+      k_stride % 8 || v_stride < kv_row || v_stride % 8)
+    return TV_ERR_INVALID_ARG;
+  tv::MropeArgs a{};
+  a.q_out = static_cast<__nv_bfloat16*>(q_out);
+  a.q = static_cast<const __nv_bfloat16*>(q);
+  a.k_new = static_cast<const __nv_bfloat16*>(k_new);
+  a.v_new = static_cast<const __nv_bfloat16*>(v_new);
+  a.q_stride = q_stride;
+  a.k_stride = k_stride;
+  a.v_stride = v_stride;
+  a.slot_mapping = slot_mapping;
+  a.positions = positions;
+  a.pair_axis = pair_axis;
+  a.num_tokens = num_tokens;
+  a.k_pool = static_cast<__nv_bfloat16*>(k_pool);
+  a.v_pool = static_cast<__nv_bfloat16*>(v_pool);
+  a.num_slots = num_pages * page_size;
+  a.cos_sin = rope_cos_sin;
+  a.err = err;
+  a.num_axes = num_axes;
+  a.max_position = rope_max_position;
+  a.num_q_heads = q ? num_q_heads : 0;
+  a.num_kv_heads = num_kv_heads;
+  return cuda_status(
+      tv::launch_kv_append_mrope(a, static_cast<cudaStream_t>(stream)));
+}
+
 // Device workspace of the work-balanced decode: per-item counters, then two
 // partial-result slots per warp of the persistent grid.
 struct BalancedWorkspace {
@@ -505,6 +560,78 @@ tv_status tv_pool_release(int32_t* pool_state, int64_t num_pages,
       static_cast<cudaStream_t>(stream)));
 }
 
+tv_status tv_pool_truncate(int32_t* pool_state, int64_t num_pages,
+                           int32_t* block_tables, int max_blocks_per_seq,
+                           int32_t* context_lens, const int32_t* new_lens,
+                           int num_seqs, uint32_t* err, void* stream) {
+  tv_status st = pool_common(pool_state, num_pages, block_tables,
+                             max_blocks_per_seq, context_lens, num_seqs);
+  if (st != TV_OK) return st;
+  if (num_seqs == 0) return TV_OK;
+  if (!new_lens) return TV_ERR_INVALID_ARG;
+  return cuda_status(tv::launch_pool_truncate(
+      pool_state, (int)num_pages, block_tables, max_blocks_per_seq,
+      context_lens, new_lens, num_seqs, err,
+      static_cast<cudaStream_t>(stream)));
+}
+
+// What both calls that move whole pages need of the pools.
+static tv_status check_pools(const void* k_pool, const void* v_pool,
+                             int64_t num_pages, int num_kv_heads, int head_dim,
+                             int page_size) {
+  if (head_dim != kHeadDim || !page_size_ok(page_size))
+    return TV_ERR_UNSUPPORTED;
+  if (num_kv_heads <= 0 || num_pages <= 0 || !aligned16(k_pool) ||
+      !aligned16(v_pool))
+    return TV_ERR_INVALID_ARG;
+  // the bytes of a page are counted in an int
+  if (num_pages * page_size > INT32_MAX ||
+      (int64_t)page_size * num_kv_heads * head_dim * 2 > INT32_MAX)
+    return TV_ERR_UNSUPPORTED;
+  return TV_OK;
+}
+
+tv_status tv_pool_compact(int32_t* pool_state, int64_t num_pages,
+                          int32_t* block_tables, int max_blocks_per_seq,
+                          const int32_t* context_lens, int num_seqs,
+                          int32_t* move_src, int32_t* move_dst,
+                          int64_t max_moves, int32_t* num_moves, void* k_pool,
+                          void* v_pool, int num_kv_heads, int head_dim,
+                          int page_size, uint32_t* err, void* stream) {
+  tv_status st = pool_common(pool_state, num_pages, block_tables,
+                             max_blocks_per_seq, context_lens, num_seqs);
+  if (st != TV_OK) return st;
+  st = check_pools(k_pool, v_pool, num_pages, num_kv_heads, head_dim,
+                   page_size);
+  if (st != TV_OK) return st;
+  if (!move_src || !move_dst || !num_moves || max_moves < num_pages / 2 ||
+      (k_pool != nullptr) != (v_pool != nullptr))
+    return TV_ERR_INVALID_ARG;
+  return cuda_status(tv::launch_pool_compact(
+      pool_state, (int)num_pages, page_size, block_tables, max_blocks_per_seq,
+      context_lens, num_seqs, move_src, move_dst, num_moves, k_pool, v_pool,
+      num_kv_heads * head_dim * 2, err, static_cast<cudaStream_t>(stream)));
+}
+
+tv_status tv_page_copy(void* k_pool, void* v_pool, int64_t num_pages,
+                       const int32_t* src_pages, const int32_t* dst_pages,
+                       int64_t max_pairs, const int32_t* num_pairs,
+                       int num_kv_heads, int head_dim, int page_size,
+                       uint32_t* err, void* stream) {
+  tv_status st = check_pools(k_pool, v_pool, num_pages, num_kv_heads, head_dim,
+                             page_size);
+  if (st != TV_OK) return st;
+  if (max_pairs < 0) return TV_ERR_INVALID_ARG;
+  if (max_pairs > INT32_MAX) return TV_ERR_UNSUPPORTED;
+  if (max_pairs == 0) return TV_OK;
+  if (!k_pool || !v_pool || !src_pages || !dst_pages)
+    return TV_ERR_INVALID_ARG;
+  return cuda_status(tv::launch_page_copy(
+      k_pool, v_pool, (int)num_pages, page_size * num_kv_heads * head_dim * 2,
+      src_pages, dst_pages, max_pairs, num_pairs, err,
+      static_cast<cudaStream_t>(stream)));
+}
+
 tv_status tv_decode_step(int32_t* pool_state, int64_t num_pages, void* out,
                          const void* q, const void* k_new, const void* v_new,
                          void* k_pool, void* v_pool, int32_t* block_tables,
@@ -668,6 +795,121 @@ tv_status tv_paged_prefill(void* out, const void* q, int64_t num_query_rows,
   a.group = group;
   return cuda_status(tv::launch_paged_prefill(
       a, tq, tk, tvm, static_cast<cudaStream_t>(stream)));
+}
+
+// ---- attention of a chunk of rows per sequence -----------------------------------
+
+static size_t chunk_workspace_bytes(int, int, int, int) { return 0; }
+
+tv_status tv_chunk_workspace_size(int num_seqs, int max_query_len,
+                                  int num_q_heads, int num_kv_heads,
+                                  int head_dim, size_t* bytes) {
+  tv_status st =
+      check_attention_shape(num_q_heads, num_kv_heads, head_dim, kPageSize);
+  if (st != TV_OK) return st;
+  if (!bytes || num_seqs < 0 || max_query_len < 0) return TV_ERR_INVALID_ARG;
+  *bytes = chunk_workspace_bytes(num_seqs, max_query_len, num_q_heads,
+                                 num_kv_heads);
+  return TV_OK;
+}
+
+static tv_status chunk_common(void* out, const void* q, int64_t num_query_rows,
+                              const int32_t* query_start_loc,
+                              const void* k_pool, const void* v_pool,
+                              const int32_t* block_tables,
+                              int max_blocks_per_seq,
+                              const int32_t* context_lens, int num_seqs,
+                              int max_query_len, int num_q_heads,
+                              int num_kv_heads, int head_dim, int page_size,
+                              int64_t num_pages, float scale, void* workspace,
+                              size_t workspace_bytes, bool causal,
+                              uint32_t* err, void* stream) {
+  tv_status st =
+      check_attention_shape(num_q_heads, num_kv_heads, head_dim, page_size);
+  if (st != TV_OK) return st;
+  // the kernels scale each tile's maximum raw score, which is the maximum
+  // of the scaled scores only when the scale is positive
+  if (num_seqs < 0 || max_blocks_per_seq <= 0 || num_pages <= 0 ||
+      max_query_len < 0 || num_query_rows < 0 || !std::isfinite(scale) ||
+      !(scale > 0.f))
+    return TV_ERR_INVALID_ARG;
+  if (num_seqs > 65535 || num_pages * page_size > INT32_MAX ||
+      (int64_t)max_blocks_per_seq * page_size > INT32_MAX ||
+      num_query_rows > INT32_MAX)
+    return TV_ERR_UNSUPPORTED;
+  const int group = num_q_heads / num_kv_heads;
+  if ((int64_t)max_query_len * group > 65535ll * 16) return TV_ERR_UNSUPPORTED;
+  if (num_seqs == 0 || max_query_len == 0 || num_query_rows == 0)
+    return TV_OK;
+  if (!out || !q || !query_start_loc || !k_pool || !v_pool || !block_tables ||
+      !context_lens)
+    return TV_ERR_INVALID_ARG;
+  if (!aligned16(out) || !aligned16(q) || !aligned16(k_pool) ||
+      !aligned16(v_pool))
+    return TV_ERR_INVALID_ARG;
+  if (workspace && (!aligned16(workspace) ||
+                    workspace_bytes <
+                        chunk_workspace_bytes(num_seqs, max_query_len,
+                                              num_q_heads, num_kv_heads)))
+    return TV_ERR_INVALID_ARG;
+
+  CUtensorMap tk, tvm;
+  st = pool_tensor_map(&tk, k_pool, num_pages, page_size, num_kv_heads,
+                       CU_TENSOR_MAP_SWIZZLE_128B);
+  if (st != TV_OK) return st;
+  st = pool_tensor_map(&tvm, v_pool, num_pages, page_size, num_kv_heads,
+                       CU_TENSOR_MAP_SWIZZLE_128B);
+  if (st != TV_OK) return st;
+  tv::ChunkArgs a{};
+  a.out = static_cast<__nv_bfloat16*>(out);
+  a.q = static_cast<const __nv_bfloat16*>(q);
+  a.query_start_loc = query_start_loc;
+  a.block_tables = block_tables;
+  a.context_lens = context_lens;
+  a.err = err;
+  a.max_blocks_per_seq = max_blocks_per_seq;
+  a.num_seqs = num_seqs;
+  a.num_q_heads = num_q_heads;
+  a.num_kv_heads = num_kv_heads;
+  a.num_pages = static_cast<int>(num_pages);
+  a.max_query_len = max_query_len;
+  a.num_query_rows = num_query_rows;
+  a.scale_log2 = scale * 1.4426950408889634f;
+  a.page_shift = page_shift(page_size);
+  a.group_shift = group == 8 ? 3 : group >> 1;
+  return cuda_status(tv::launch_paged_chunk(
+      a, tk, tvm, causal, static_cast<cudaStream_t>(stream)));
+}
+
+tv_status tv_paged_chunk(void* out, const void* q, int64_t num_query_rows,
+                         const int32_t* query_start_loc, const void* k_pool,
+                         const void* v_pool, const int32_t* block_tables,
+                         int max_blocks_per_seq, const int32_t* context_lens,
+                         int num_seqs, int max_query_len, int num_q_heads,
+                         int num_kv_heads, int head_dim, int page_size,
+                         int64_t num_pages, float scale, void* workspace,
+                         size_t workspace_bytes, uint32_t* err,
+                         void* stream) {
+  return chunk_common(out, q, num_query_rows, query_start_loc, k_pool, v_pool,
+                      block_tables, max_blocks_per_seq, context_lens, num_seqs,
+                      max_query_len, num_q_heads, num_kv_heads, head_dim,
+                      page_size, num_pages, scale, workspace, workspace_bytes,
+                      true, err, stream);
+}
+
+tv_status tv_paged_cross_attention(
+    void* out, const void* q, int64_t num_query_rows,
+    const int32_t* query_start_loc, const void* k_pool, const void* v_pool,
+    const int32_t* block_tables, int max_blocks_per_seq,
+    const int32_t* encoder_lens, int num_seqs, int max_query_len,
+    int num_q_heads, int num_kv_heads, int head_dim, int page_size,
+    int64_t num_pages, float scale, void* workspace, size_t workspace_bytes,
+    uint32_t* err, void* stream) {
+  return chunk_common(out, q, num_query_rows, query_start_loc, k_pool, v_pool,
+                      block_tables, max_blocks_per_seq, encoder_lens, num_seqs,
+                      max_query_len, num_q_heads, num_kv_heads, head_dim,
+                      page_size, num_pages, scale, workspace, workspace_bytes,
+                      false, err, stream);
 }
 
 }  // extern "C"

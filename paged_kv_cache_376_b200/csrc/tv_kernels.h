@@ -81,6 +81,23 @@ cudaError_t launch_pool_release(int32_t* state, int num_pages, int32_t* bt,
                                 const int32_t* seqs, int num_release,
                                 uint32_t* err, cudaStream_t stream);
 
+cudaError_t launch_pool_truncate(int32_t* state, int num_pages, int32_t* bt,
+                                 int mb, int32_t* ctx, const int32_t* new_lens,
+                                 int num_seqs, uint32_t* err,
+                                 cudaStream_t stream);
+// Pools may be null (tables and moves only).
+cudaError_t launch_pool_compact(int32_t* state, int num_pages, int page_size,
+                                int32_t* bt, int mb, const int32_t* ctx,
+                                int num_seqs, int32_t* move_src,
+                                int32_t* move_dst, int32_t* num_moves,
+                                void* k_pool, void* v_pool, int row_bytes,
+                                uint32_t* err, cudaStream_t stream);
+cudaError_t launch_page_copy(void* k_pool, void* v_pool, int num_pages,
+                             int page_bytes, const int32_t* src,
+                             const int32_t* dst, int64_t max_pairs,
+                             const int32_t* num_pairs, uint32_t* err,
+                             cudaStream_t stream);
+
 // Bounded-wait self-test (selftest.cu).
 cudaError_t launch_wait_selftest(uint32_t* err, unsigned long long limit_ns,
                                  unsigned long long* waited_ns,
@@ -94,6 +111,28 @@ cudaError_t launch_kv_append_rope(const void* k_new, const void* v_new,
                                   const float* rope_cos_sin,
                                   int rope_max_position, uint32_t* err,
                                   cudaStream_t stream);
+
+struct MropeArgs {
+  __nv_bfloat16* q_out;          // [T][Hq][D], null: K and V only
+  const __nv_bfloat16* q;        // token t at q + t * q_stride
+  const __nv_bfloat16* k_new;
+  const __nv_bfloat16* v_new;
+  int64_t q_stride, k_stride, v_stride;   // elements between tokens
+  const int32_t* slot_mapping;   // [T]
+  const int32_t* positions;      // [num_axes][T]
+  const int32_t* pair_axis;      // [D / 2]
+  int64_t num_tokens;
+  __nv_bfloat16* k_pool;
+  __nv_bfloat16* v_pool;
+  int64_t num_slots;
+  const float* cos_sin;          // [max_position][2][D / 2]
+  uint32_t* err;
+  int num_axes;
+  int max_position;
+  int num_q_heads;               // 0 when q_out is null
+  int num_kv_heads;
+};
+cudaError_t launch_kv_append_mrope(const MropeArgs& a, cudaStream_t stream);
 
 cudaError_t launch_kv_append(const void* k_new, const void* v_new,
                              const int32_t* slot_mapping, int64_t num_tokens,
@@ -144,5 +183,29 @@ __host__ __device__ inline int prefill_blocks(int max_query_len, int group) {
 cudaError_t launch_paged_prefill(const PrefillArgs& a, const CUtensorMap& tq,
                                  const CUtensorMap& tk, const CUtensorMap& tv,
                                  cudaStream_t stream);
+
+// Attention of a chunk of rows per sequence (paged_chunk.cu).
+struct ChunkArgs {
+  __nv_bfloat16* out;            // [rows][Hq][D]
+  const __nv_bfloat16* q;        // [rows][Hq][D]
+  const int32_t* query_start_loc;  // [B+1]
+  const int32_t* block_tables;
+  const int32_t* context_lens;
+  uint32_t* err;
+  int max_blocks_per_seq;
+  int num_seqs;
+  int num_q_heads;
+  int num_kv_heads;
+  int num_pages;
+  int max_query_len;
+  int64_t num_query_rows;
+  float scale_log2;
+  int page_shift;                // page_size = 16 << page_shift
+  int group_shift;               // query heads per KV head = 1 << group_shift
+};
+
+cudaError_t launch_paged_chunk(const ChunkArgs& a, const CUtensorMap& tk,
+                               const CUtensorMap& tv, bool causal,
+                               cudaStream_t stream);
 
 }  // namespace tv
