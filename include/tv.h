@@ -410,8 +410,9 @@ tv_status tv_prefill_workspace_size(int num_seqs, int max_query_len,
  *                    as they were; a sequence may have no rows
  *   max_query_len    >= every T_s
  *   workspace        NULL (keys are not split), or device memory of at least
- *                    tv_chunk_workspace_size() bytes, 16-byte aligned, no
- *                    initial contents needed.  Calls that overlap on the GPU
+ *                    tv_chunk_workspace_size() bytes, 16-byte aligned, zeroed
+ *                    once before its first use (every call leaves its
+ *                    counters at zero again).  Calls that overlap on the GPU
  *                    need separate workspaces.
  *   workspace_bytes  its size; too small returns TV_ERR_INVALID_ARG
  * A sequence with T_s > C, T_s > max_query_len or rows outside q is flagged

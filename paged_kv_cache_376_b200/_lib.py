@@ -418,7 +418,7 @@ def prefill_workspace(num_seqs, max_query_len, device="cuda"):
     """Device workspace for the cost-ordered prefill dispatch (no initial
     contents needed)."""
     n = tv_prefill_workspace_size(num_seqs, max_query_len)
-    return torch.empty(max(n, 16), dtype=torch.uint8, device=device)
+    return torch.zeros(max(n, 16), dtype=torch.uint8, device=device)
 
 
 def tv_paged_prefill(out, q, query_start_loc, k_pool, v_pool, block_tables,
@@ -471,13 +471,13 @@ def tv_chunk_workspace_size(num_seqs, max_query_len, num_q_heads,
 
 def chunk_workspace(num_seqs, max_query_len, num_q_heads, num_kv_heads,
                     device=None):
-    """Workspace of tv_paged_chunk / tv_paged_cross_attention (no initial
-    contents needed)."""
+    """Zeroed workspace of tv_paged_chunk / tv_paged_cross_attention (every
+    call leaves its counters at zero again)."""
     device = torch.device(device or "cuda")
     with torch.cuda.device(device):
         n = tv_chunk_workspace_size(num_seqs, max_query_len, num_q_heads,
                                     num_kv_heads)
-        return torch.empty(max(n, 16), dtype=torch.uint8, device=device)
+        return torch.zeros(max(n, 16), dtype=torch.uint8, device=device)
 
 
 def _chunk(name, out, q, query_start_loc, k_pool, v_pool, block_tables, lens,

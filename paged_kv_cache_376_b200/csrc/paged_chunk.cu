@@ -33,22 +33,31 @@ constexpr int kD = 64;
 constexpr int kPS = 16;          // tokens per TMA box
 constexpr int kWarps = 4;
 constexpr int kThreads = kWarps * 32;
+constexpr int kStages = 3;       // boxes of K and V in flight per warp
 constexpr int kRowBytes = kD * 2;
 constexpr int kSliceBytes = kPS * kRowBytes;
 constexpr int kStageBytes = 2 * kSliceBytes;
 constexpr float kLazy = 8.f;     // log2 of the growth the running sums allow
 
-template <int MB, int kStages>
-struct ChunkSmem {
-  alignas(1024) uint8_t ring[kWarps][kStages][kStageBytes];
+struct ChunkRing {
+  alignas(1024) uint8_t slot[kWarps][kStages][kStageBytes];
   alignas(8) uint64_t full[kWarps][kStages];
 };
 
-template <int MB>
-struct ChunkCombine {   // per-warp results handed to the final combine
-  float m[kWarps][16 * MB];
-  float l[kWarps][16 * MB];
-  float acc[kWarps][16 * MB][kD];
+// Per-warp results of 16 rows, handed to the combine (rows padded so that the
+// lanes of a fragment hit different banks).
+struct ChunkCombine {
+  float m[kWarps][16];
+  float l[kWarps][16];
+  alignas(16) float acc[kWarps][16][kD + 8];
+};
+
+// The rows of one sequence that a CTA works on, and the keys they see.
+struct ChunkRows {
+  int q_row;          // first query row in q / out
+  int tb;             // query rows
+  int first_limit;    // last key that the first row sees
+  int key_end;        // keys that some row sees: [0, key_end)
 };
 
 // A weight of zero does not hide an infinity or a NaN in V.  On a page of
@@ -97,173 +106,79 @@ __device__ __forceinline__ void part_visible_nonfinite(
   __syncwarp();
 }
 
-template <int MB, int kStages, bool kCausal>
-__global__ void __launch_bounds__(kThreads, MB == 1 ? 4 : 3)
-    paged_chunk_kernel(const ChunkArgs a,
-                       const __grid_constant__ CUtensorMap tm_k,
-                       const __grid_constant__ CUtensorMap tm_v) {
-  constexpr int kRows = 16 * MB;
-  static_assert(sizeof(ChunkCombine<MB>) <=
-                    sizeof(ChunkSmem<MB, kStages>::ring),
-                "combine buffer must fit in the ring");
-  extern __shared__ __align__(1024) uint8_t smem_dyn[];
-  uint8_t* smem_raw = smem_dyn + ((1024 - (smem_u32(smem_dyn) & 1023)) & 1023);
-  auto& sm = *reinterpret_cast<ChunkSmem<MB, kStages>*>(smem_raw);
-
-  const int kvh = blockIdx.x;
-  const int seq = blockIdx.y;
-  const int blk = blockIdx.z;
-  const int warp = threadIdx.x >> 5;
-  const int lane = threadIdx.x & 31;
-  const int G = 1 << a.group_shift;
-
-  // ---- rows and keys of this CTA ---------------------------------------------
-  const int qs = a.query_start_loc[seq];
-  const int T = a.query_start_loc[seq + 1] - qs;
-  int ctx = a.context_lens[seq];
-  const int t0 = blk * (kRows >> a.group_shift);   // first query row
-  const int ctx_cap = a.max_blocks_per_seq * (kPS << a.page_shift);
-  const bool head_cta = threadIdx.x == 0 && blk == 0 && kvh == 0;
-  if (ctx < 0 || ctx > ctx_cap) {
-    if (head_cta) flag_error(a.err, DEVERR_BAD_CONTEXT);
-    ctx = ctx < 0 ? 0 : ctx_cap;
-  }
-  if (T < 0 || T > a.max_query_len || qs < 0 ||
-      (int64_t)qs + T > a.num_query_rows || (kCausal && T > ctx)) {
-    if (head_cta) flag_error(a.err, DEVERR_BAD_QUERY);
-    return;
-  }
-  if (t0 >= T) return;
-  const int tb = min(kRows >> a.group_shift, T - t0);   // query rows here
-  const int rows = tb << a.group_shift;
-  const int first_limit = kCausal ? ctx - T + t0 : ctx - 1;  // row 0's last key
-  const int key_end = kCausal ? first_limit + tb : ctx;
-  const int n_pages = (key_end + kPS - 1) / kPS;
-  const int my_n = n_pages > warp ? (n_pages - warp + kWarps - 1) / kWarps : 0;
-  const int32_t* bt = a.block_tables + (size_t)seq * a.max_blocks_per_seq;
-  const int sub_mask = (1 << a.page_shift) - 1;
-
-  if (lane == 0) {
-    for (int s = 0; s < kStages; ++s) mbar_init(smem_u32(&sm.full[warp][s]), 1);
-    fence_mbar_init();
-  }
-  __syncwarp();
-
-  // Pool blocks of this warp's 16-token blocks, 32 per batch, one per lane
-  // (-1 when the block-table entry is not a page of the pool).
-  auto load_pids = [&](int batch) -> int {
-    const int i = batch * 32 + lane;
-    if (i >= my_n) return -1;
-    const int b = warp + kWarps * i;
-    const int page = __ldg(bt + (b >> a.page_shift));
-    return page >= 0 && page < a.num_pages
-               ? (page << a.page_shift) + (b & sub_mask) : -1;
-  };
-  const uint64_t policy = l2_policy_evict_first();
-  auto issue = [&](int pid, int stage) {
-    if (pid < 0) flag_error(a.err, DEVERR_BAD_PAGE);
-    const int y = (pid < 0 ? 0 : pid) * kPS;
-    const uint32_t bar = smem_u32(&sm.full[warp][stage]);
-    const uint32_t dst = smem_u32(&sm.ring[warp][stage][0]);
-    mbar_arrive_expect_tx(bar, kStageBytes);
-    tma_load_2d_hint(dst, &tm_k, kvh * kD, y, bar, policy);
-    tma_load_2d_hint(dst + kSliceBytes, &tm_v, kvh * kD, y, bar, policy);
-  };
-  int pid_cur = load_pids(0), pid_next = load_pids(1);
-#pragma unroll
-  for (int j = 0; j < kStages; ++j) {
-    const int pid = __shfl_sync(0xffffffffu, pid_cur, j);
-    if (lane == 0 && j < my_n) issue(pid, j);
-  }
-
-  // ---- fragments ---------------------------------------------------------------
-  // Lane 4g + c.  Rows g and g + 8 of each 16-row block are the lane's; as
-  // the A operand of S = Q K^T it holds dims 16k + 2c, +1 and + 8 of them.
-  const int g = lane >> 2;
-  const int c = lane & 3;
+// What a warp holds of 16 MB rows: q, the running offset and sum of each row
+// and the accumulators.  Lane 4g + c owns rows g and g + 8 of each 16-row
+// block, and in the accumulators dims 8d + 2c, +1 of them.
+template <int MB, bool kCausal>
+struct WarpRows {
   uint32_t qa[MB][4][4];
-  int limit[MB][2];
-#pragma unroll
-  for (int b = 0; b < MB; ++b) {
-#pragma unroll
-    for (int e = 0; e < 2; ++e) {
-      const int r = 16 * b + g + 8 * e;
-      const bool real = r < rows;
-      const int t = r >> a.group_shift, h = r & (G - 1);
-      const uint32_t* src = reinterpret_cast<const uint32_t*>(
-          a.q + ((size_t)(qs + t0 + (real ? t : 0)) * a.num_q_heads +
-                 kvh * G + (real ? h : 0)) * kD);
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        qa[b][k][e] = real ? __ldg(src + 8 * k + c) : 0u;
-        qa[b][k][e + 2] = real ? __ldg(src + 8 * k + c + 4) : 0u;
-      }
-      limit[b][e] = kCausal ? first_limit + (real ? t : tb - 1) : ctx - 1;
-    }
-  }
-  // ldmatrix row addresses inside a swizzled 2 KB slice (16-byte chunk j of
-  // row r at chunk j ^ (r & 7)).  K: (rows 0-7 | 8-15) x (chunk 2k | 2k + 1),
-  // V (transposed): (chunk 2t | 2t + 1) x (rows 0-7 | 8-15).
-  uint32_t koff[4], voff[4];
-  {
-    const int mi = lane >> 3, r7 = lane & 7;
-    const int kr = r7 + 8 * (mi >> 1), vr = r7 + 8 * (mi & 1);
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      koff[k] = kr * kRowBytes + (((2 * k + (mi & 1)) ^ r7) << 4);
-      voff[k] = vr * kRowBytes + (((2 * k + (mi >> 1)) ^ r7) << 4);
-    }
-  }
-
+  int limit[MB][2];      // last key that the row sees
   float m[MB][2], l[MB][2], acc[MB][8][4];
-#pragma unroll
-  for (int b = 0; b < MB; ++b) {
-    m[b][0] = m[b][1] = -INFINITY;
-    l[b][0] = l[b][1] = 0.f;
-#pragma unroll
-    for (int n = 0; n < 8; ++n)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) acc[b][n][e] = 0.f;
-  }
-  const float sl = a.scale_log2;
 
-  bool failed = false;
-  int issued = min(my_n, kStages);
-  int i = 0;
-  for (; i < my_n; ++i) {
-    const int stage = i % kStages;
-    if ((i & 31) == 0 && i > 0) {
-      pid_cur = pid_next;
-      pid_next = load_pids((i >> 5) + 1);
+  __device__ __forceinline__ void clear() {
+#pragma unroll
+    for (int b = 0; b < MB; ++b) {
+      m[b][0] = m[b][1] = -INFINITY;
+      l[b][0] = l[b][1] = 0.f;
+#pragma unroll
+      for (int n = 0; n < 8; ++n)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) acc[b][n][e] = 0.f;
     }
-    const bool page_ok = __shfl_sync(0xffffffffu, pid_cur, i & 31) >= 0;
-    const int tok0 = (warp + kWarps * i) * kPS;
-    // warp-uniform: every row sees every token of the page
-    const bool full_page = page_ok && tok0 + kPS - 1 <= first_limit;
-    if (!__all_sync(0xffffffffu, mbar_wait(smem_u32(&sm.full[warp][stage]),
-                                           (i / kStages) & 1))) {
-      failed = true;
-      break;
-    }
-    uint8_t* kbase = &sm.ring[warp][stage][0];
+  }
+
+  // As the A operand of S = Q K^T a lane holds dims 16k + 2c, +1 and + 8.
+  __device__ __forceinline__ void load(const ChunkArgs& a, const ChunkRows& w,
+                                       int kvh, int lane) {
+    const int g = lane >> 2, c = lane & 3;
+    const int G = 1 << a.group_shift;
+    const int rows = w.tb << a.group_shift;
+#pragma unroll
+    for (int b = 0; b < MB; ++b)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const int r = 16 * b + g + 8 * e;
+        const bool real = r < rows;
+        const int t = real ? r >> a.group_shift : w.tb - 1;
+        const int h = r & (G - 1);
+        const uint32_t* src = reinterpret_cast<const uint32_t*>(
+            a.q + ((size_t)(w.q_row + t) * a.num_q_heads + kvh * G + h) * kD);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          qa[b][k][e] = real ? __ldg(src + 8 * k + c) : 0u;
+          qa[b][k][e + 2] = real ? __ldg(src + 8 * k + c + 4) : 0u;
+        }
+        limit[b][e] = kCausal ? w.first_limit + t : w.key_end - 1;
+      }
+  }
+
+  // One 16-token page that lies in a ring slot: tokens tok0 .. tok0 + 15.
+  __device__ __forceinline__ void page(uint8_t* kbase, int tok0, bool page_ok,
+                                       const ChunkRows& w,
+                                       const uint32_t (&koff)[4],
+                                       const uint32_t (&voff)[4], float sl,
+                                       int lane) {
+    const int c = lane & 3;
     uint8_t* vbase = kbase + kSliceBytes;
-    if (!page_ok || tok0 + kPS > key_end) {
+    // warp-uniform: every row sees every token of the page
+    const bool full_page = page_ok && tok0 + kPS - 1 <= w.first_limit;
+    if (!page_ok || tok0 + kPS > w.key_end) {
       // tokens that no row of the block sees (stale slots may hold NaN, and
       // 0 * NaN would reach the sum) and bad pages: zero V rows
 #pragma unroll
       for (int e = lane; e < kPS * 8; e += 32) {
         const int r = e >> 3;
-        if (!(page_ok && tok0 + r < key_end))
+        if (!(page_ok && tok0 + r < w.key_end))
           *reinterpret_cast<uint4*>(vbase + r * kRowBytes + (e & 7) * 16) =
               make_uint4(0, 0, 0, 0);
       }
       __syncwarp();
     }
     if (kCausal && page_ok && !full_page)
-      part_visible_nonfinite(vbase, tok0, first_limit, lane, limit, acc);
+      part_visible_nonfinite(vbase, tok0, w.first_limit, lane, limit, acc);
     const uint32_t kb = smem_u32(kbase), vb = smem_u32(vbase);
 
-    // ---- S = Q K^T: 16 MB rows x 16 tokens ------------------------------------
+    // ---- S = Q K^T: 16 MB rows x 16 tokens ----------------------------------
     float s[MB][2][4];
 #pragma unroll
     for (int b = 0; b < MB; ++b)
@@ -358,49 +273,25 @@ __global__ void __launch_bounds__(kThreads, MB == 1 ? 4 : 3)
         mma_bf16_16816(acc[b][2 * t + 1], pl[b], vf[2], vf[3]);
       }
     }
-
-    // ---- hand the slot back to the TMA unit ------------------------------------
-    fence_proxy_async_smem();
-    __syncwarp();
-    const int j = i + kStages;
-    const int src = ((j >> 5) == (i >> 5)) ? pid_cur : pid_next;
-    const int pid_j = __shfl_sync(0xffffffffu, src, j & 31);
-    if (j < my_n) {
-      if (lane == 0) issue(pid_j, stage);
-      ++issued;
-    }
   }
-  if (failed) {
-    // let the copies in flight land (bounded), then an empty result
-    if (lane == 0) flag_error(a.err, DEVERR_TIMEOUT);
-    for (int k = i; k < issued; ++k)
-      mbar_wait(smem_u32(&sm.full[warp][k % kStages]), (k / kStages) & 1);
+
+  // The quads hold a row's sum in four parts.
+  __device__ __forceinline__ void finish_sums() {
 #pragma unroll
     for (int b = 0; b < MB; ++b)
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
-        m[b][e] = -INFINITY;
-        l[b][e] = 0.f;
-#pragma unroll
-        for (int d = 0; d < 8; ++d) acc[b][d][2 * e] = acc[b][d][2 * e + 1] = 0.f;
+        l[b][e] += __shfl_xor_sync(0xffffffffu, l[b][e], 1);
+        l[b][e] += __shfl_xor_sync(0xffffffffu, l[b][e], 2);
       }
   }
 
-  // ---- combine the four warps and write -----------------------------------------
-#pragma unroll
-  for (int b = 0; b < MB; ++b)
-#pragma unroll
-    for (int e = 0; e < 2; ++e) {
-      l[b][e] += __shfl_xor_sync(0xffffffffu, l[b][e], 1);
-      l[b][e] += __shfl_xor_sync(0xffffffffu, l[b][e], 2);
-    }
-  __syncthreads();   // every warp is done with its ring
-  auto& cb = *reinterpret_cast<ChunkCombine<MB>*>(smem_raw);
-#pragma unroll
-  for (int b = 0; b < MB; ++b)
+  __device__ __forceinline__ void put(ChunkCombine& cb, int b, int warp,
+                                      int lane) const {
+    const int g = lane >> 2, c = lane & 3;
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
-      const int r = 16 * b + g + 8 * e;
+      const int r = g + 8 * e;
 #pragma unroll
       for (int d = 0; d < 8; ++d)
         *reinterpret_cast<float2*>(&cb.acc[warp][r][8 * d + 2 * c]) =
@@ -410,43 +301,535 @@ __global__ void __launch_bounds__(kThreads, MB == 1 ? 4 : 3)
         cb.l[warp][r] = l[b][e];
       }
     }
-  __syncthreads();
-  for (int o = threadIdx.x; o < rows * (kD / 2); o += kThreads) {
-    const int r = o / (kD / 2), d = 2 * (o % (kD / 2));
-    float M = -INFINITY;
-#pragma unroll
-    for (int w = 0; w < kWarps; ++w) M = fmaxf(M, cb.m[w][r]);
-    float L = 0.f, x = 0.f, y = 0.f;
-#pragma unroll
-    for (int w = 0; w < kWarps; ++w) {
-      // equal offsets first: -inf (no finite score) must not become NaN
-      const float f = cb.m[w][r] == M ? 1.f : fast_exp2(cb.m[w][r] - M);
-      const float2 v = *reinterpret_cast<const float2*>(&cb.acc[w][r][d]);
-      L = fmaf(cb.l[w][r], f, L);
-      x = fmaf(v.x, f, x);
-      y = fmaf(v.y, f, y);
-    }
-    const float inv = L == 0.f ? 0.f : 1.f / L;   // NaN scores stay NaN
-    const size_t row = (size_t)(qs + t0 + (r >> a.group_shift)) *
-                           a.num_q_heads + kvh * G + (r & (G - 1));
-    *reinterpret_cast<uint32_t*>(a.out + row * kD + d) =
-        pack_bf16x2(x * inv, y * inv);
   }
+};
+
+// Joins partial results (offset m, sum l, unscaled output) of 8 dims of one
+// row, dims 4k .. 4k + 3 and 32 + 4k .. : any common offset gives the same
+// ratio, and the order of the parts is fixed.
+struct Joined {
+  float M = -INFINITY, L = 0.f;
+  float4 x = make_float4(0.f, 0.f, 0.f, 0.f), y = x;
+  __device__ __forceinline__ void add(float m, float l, float4 u, float4 v) {
+    // equal offsets first: -inf (no finite score) must not become NaN
+    const float f = m == M ? 1.f : fast_exp2(m - M);
+    L = fmaf(l, f, L);
+    x.x = fmaf(u.x, f, x.x);
+    x.y = fmaf(u.y, f, x.y);
+    x.z = fmaf(u.z, f, x.z);
+    x.w = fmaf(u.w, f, x.w);
+    y.x = fmaf(v.x, f, y.x);
+    y.y = fmaf(v.y, f, y.y);
+    y.z = fmaf(v.z, f, y.z);
+    y.w = fmaf(v.w, f, y.w);
+  }
+  __device__ __forceinline__ void write(__nv_bfloat16* row, int k) const {
+    const float inv = L == 0.f ? 0.f : 1.f / L;   // NaN scores stay NaN
+    *reinterpret_cast<uint2*>(row + 4 * k) = make_uint2(
+        pack_bf16x2(x.x * inv, x.y * inv), pack_bf16x2(x.z * inv, x.w * inv));
+    *reinterpret_cast<uint2*>(row + 32 + 4 * k) = make_uint2(
+        pack_bf16x2(y.x * inv, y.y * inv), pack_bf16x2(y.z * inv, y.w * inv));
+  }
+};
+
+__device__ __forceinline__ Joined join_warps(const ChunkCombine& cb, int r,
+                                             int k) {
+  Joined j;
+#pragma unroll
+  for (int w = 0; w < kWarps; ++w) j.M = fmaxf(j.M, cb.m[w][r]);
+#pragma unroll
+  for (int w = 0; w < kWarps; ++w)
+    j.add(cb.m[w][r], cb.l[w][r],
+          *reinterpret_cast<const float4*>(&cb.acc[w][r][4 * k]),
+          *reinterpret_cast<const float4*>(&cb.acc[w][r][32 + 4 * k]));
+  return j;
+}
+
+// Row r of a CTA's rows in the output.
+__device__ __forceinline__ __nv_bfloat16* out_row(const ChunkArgs& a,
+                                                  int q_row, int kvh, int r) {
+  return a.out + ((size_t)(q_row + (r >> a.group_shift)) * a.num_q_heads +
+                  (kvh << a.group_shift) + (r & ((1 << a.group_shift) - 1))) *
+                     kD;
+}
+
+// ldmatrix row addresses inside a swizzled 2 KB slice (16-byte chunk j of row r
+// at chunk j ^ (r & 7)).  K: (rows 0-7 | 8-15) x (chunk 2k | 2k + 1), V
+// (transposed): (chunk 2t | 2t + 1) x (rows 0-7 | 8-15).
+__device__ __forceinline__ void slice_offsets(int lane, uint32_t (&koff)[4],
+                                              uint32_t (&voff)[4]) {
+  const int mi = lane >> 3, r7 = lane & 7;
+  const int kr = r7 + 8 * (mi >> 1), vr = r7 + 8 * (mi & 1);
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    koff[k] = kr * kRowBytes + (((2 * k + (mi & 1)) ^ r7) << 4);
+    voff[k] = vr * kRowBytes + (((2 * k + (mi >> 1)) ^ r7) << 4);
+  }
+}
+
+// Pool block (16 rows) of 16-token block `b` of a sequence, -1 when its
+// block-table entry is not a page of the pool.
+__device__ __forceinline__ int pool_block(const ChunkArgs& a, int seq, int b) {
+  const int page = __ldg(a.block_tables + (size_t)seq * a.max_blocks_per_seq +
+                         (b >> a.page_shift));
+  return page >= 0 && page < a.num_pages
+             ? (page << a.page_shift) + (b & ((1 << a.page_shift) - 1))
+             : -1;
+}
+
+// Fills a ring slot; a bad page (-1) is flagged and block 0 loaded in its
+// place (its tokens are masked and its V rows zeroed before use).
+__device__ __forceinline__ void issue_block(const ChunkArgs& a,
+                                            const CUtensorMap* tm_k,
+                                            const CUtensorMap* tm_v, int x,
+                                            int block, uint32_t dst,
+                                            uint32_t bar, uint64_t policy) {
+  if (block < 0) flag_error(a.err, DEVERR_BAD_PAGE);
+  const int y = (block < 0 ? 0 : block) * kPS;
+  mbar_arrive_expect_tx(bar, kStageBytes);
+  tma_load_2d_hint(dst, tm_k, x, y, bar, policy);
+  tma_load_2d_hint(dst + kSliceBytes, tm_v, x, y, bar, policy);
+}
+
+// Rows and context of a sequence as the call may use them; flags what is out
+// of range when `report`.  False when the sequence has no rows to serve.
+template <bool kCausal>
+__device__ __forceinline__ bool sequence_rows(const ChunkArgs& a, int seq,
+                                              bool report, int* qs, int* T,
+                                              int* ctx) {
+  *qs = a.query_start_loc[seq];
+  *T = a.query_start_loc[seq + 1] - *qs;
+  *ctx = a.context_lens[seq];
+  const int cap = a.max_blocks_per_seq * (kPS << a.page_shift);
+  if (*ctx < 0 || *ctx > cap) {
+    if (report) flag_error(a.err, DEVERR_BAD_CONTEXT);
+    *ctx = *ctx < 0 ? 0 : cap;
+  }
+  if (*T < 0 || *T > a.max_query_len || *qs < 0 ||
+      (int64_t)*qs + *T > a.num_query_rows || (kCausal && *T > *ctx)) {
+    if (report) flag_error(a.err, DEVERR_BAD_QUERY);
+    return false;
+  }
+  return *T > 0;
+}
+
+// ---- one CTA per (KV head, block of rows, sequence) -----------------------------
+// Without a workspace, or with more sequences than the balanced kernel's
+// prefix sums hold.
+template <int MB, bool kCausal>
+__global__ void __launch_bounds__(kThreads, 3)
+    paged_chunk_kernel(const ChunkArgs a,
+                       const __grid_constant__ CUtensorMap tm_k,
+                       const __grid_constant__ CUtensorMap tm_v) {
+  static_assert(sizeof(ChunkCombine) <= sizeof(ChunkRing::slot),
+                "the combine buffer must fit in the ring");
+  extern __shared__ __align__(1024) uint8_t smem_dyn[];
+  uint8_t* smem_raw = smem_dyn + ((1024 - (smem_u32(smem_dyn) & 1023)) & 1023);
+  auto& sm = *reinterpret_cast<ChunkRing*>(smem_raw);
+
+  const int kvh = blockIdx.x;
+  const int seq = blockIdx.y;
+  const int blk = blockIdx.z;
+  const int warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31;
+  const int per_block = (16 * MB) >> a.group_shift;   // query rows
+
+  int qs, T, ctx;
+  if (!sequence_rows<kCausal>(a, seq, threadIdx.x == 0 && blk == 0 && kvh == 0,
+                              &qs, &T, &ctx))
+    return;
+  const int t0 = blk * per_block;   // first query row
+  if (t0 >= T) return;
+  ChunkRows w;
+  w.q_row = qs + t0;
+  w.tb = min(per_block, T - t0);
+  w.first_limit = kCausal ? ctx - T + t0 : ctx - 1;
+  w.key_end = kCausal ? w.first_limit + w.tb : ctx;
+  const int n_pages = (w.key_end + kPS - 1) / kPS;
+  const int my_n = n_pages > warp ? (n_pages - warp + kWarps - 1) / kWarps : 0;
+
+  if (lane == 0) {
+    for (int s = 0; s < kStages; ++s) mbar_init(smem_u32(&sm.full[warp][s]), 1);
+    fence_mbar_init();
+  }
+  __syncwarp();
+
+  // this warp's 16-token blocks, 32 per batch, one per lane
+  auto load_blocks = [&](int batch) -> int {
+    const int i = batch * 32 + lane;
+    return i < my_n ? pool_block(a, seq, warp + kWarps * i) : -1;
+  };
+  const uint64_t policy = l2_policy_evict_first();
+  auto issue = [&](int block, int stage) {
+    issue_block(a, &tm_k, &tm_v, kvh * kD, block,
+                smem_u32(&sm.slot[warp][stage][0]),
+                smem_u32(&sm.full[warp][stage]), policy);
+  };
+  int cur = load_blocks(0), next = load_blocks(1);
+#pragma unroll
+  for (int j = 0; j < kStages; ++j) {
+    const int block = __shfl_sync(0xffffffffu, cur, j);
+    if (lane == 0 && j < my_n) issue(block, j);
+  }
+
+  WarpRows<MB, kCausal> rows;
+  rows.load(a, w, kvh, lane);
+  rows.clear();
+  uint32_t koff[4], voff[4];
+  slice_offsets(lane, koff, voff);
+
+  bool failed = false;
+  int issued = min(my_n, kStages);
+  int i = 0;
+  for (; i < my_n; ++i) {
+    const int stage = i % kStages;
+    if ((i & 31) == 0 && i > 0) {
+      cur = next;
+      next = load_blocks((i >> 5) + 1);
+    }
+    const bool page_ok = __shfl_sync(0xffffffffu, cur, i & 31) >= 0;
+    if (!__all_sync(0xffffffffu, mbar_wait(smem_u32(&sm.full[warp][stage]),
+                                           (i / kStages) & 1))) {
+      failed = true;
+      break;
+    }
+    rows.page(&sm.slot[warp][stage][0], (warp + kWarps * i) * kPS, page_ok, w,
+              koff, voff, a.scale_log2, lane);
+
+    // ---- hand the slot back to the TMA unit ------------------------------------
+    fence_proxy_async_smem();
+    __syncwarp();
+    const int j = i + kStages;
+    const int src = ((j >> 5) == (i >> 5)) ? cur : next;
+    const int block = __shfl_sync(0xffffffffu, src, j & 31);
+    if (j < my_n) {
+      if (lane == 0) issue(block, stage);
+      ++issued;
+    }
+  }
+  if (failed) {
+    // let the copies in flight land (bounded), then an empty result
+    if (lane == 0) flag_error(a.err, DEVERR_TIMEOUT);
+    for (int k = i; k < issued; ++k)
+      mbar_wait(smem_u32(&sm.full[warp][k % kStages]), (k / kStages) & 1);
+    rows.clear();
+  }
+
+  // ---- combine the four warps, 16 rows at a time, and write -----------------------
+  rows.finish_sums();
+  auto& cb = *reinterpret_cast<ChunkCombine*>(smem_raw);
+  const int n_rows = w.tb << a.group_shift;
+#pragma unroll
+  for (int b = 0; b < MB; ++b) {
+    if (16 * b >= n_rows) break;
+    __syncthreads();   // every warp is done with its ring, or the last rows
+    rows.put(cb, b, warp, lane);
+    __syncthreads();
+    const int row = 16 * b + (threadIdx.x >> 3);
+    if (row < n_rows)
+      join_warps(cb, threadIdx.x >> 3, threadIdx.x & 7)
+          .write(out_row(a, w.q_row, kvh, row), threadIdx.x & 7);
+  }
+}
+
+// ---- balanced over the whole grid ------------------------------------------------
+// The blocks of 16 tokens of all sequences (those with up to 16 MB rows per KV
+// head), laid end to end, are cut into equal ranges, one per group of Hkv
+// CTAs; CTA h of a group streams KV head h of the range, so the heads of a
+// page are read at about the same time.  The grid is what is resident, so no
+// last wave runs half empty whatever the lengths, and a long context is spread
+// over as many SMs as it needs.  A boundary closer than kSnap blocks to the
+// end of a sequence moves there, so short sequences are never cut.
+//
+// A sequence inside one range is written directly.  One that is cut leaves a
+// part (m, l, unscaled output) per range in the workspace and counts up its
+// counter; the CTA that completes the count joins the parts, in the order of
+// the ranges (results do not depend on timing), and sets the counter back to
+// zero.  No CTA waits for another.
+//
+// The ring of a warp runs across sequence ends: the loads of the next
+// sequence are in flight while the last one's warps are combined.
+constexpr int kSnap = 4;
+
+struct BalancedSmem {
+  ChunkRing ring;
+  ChunkCombine cb;
+  int32_t warp_total[kWarps];
+  int32_t items;
+  int32_t last;
+  int32_t pre[kMaxChunkSeqs + 1];
+};
+
+template <int MB, bool kCausal>
+__global__ void __launch_bounds__(kThreads, 3)
+    balanced_chunk_kernel(const ChunkArgs a,
+                          const __grid_constant__ CUtensorMap tm_k,
+                          const __grid_constant__ CUtensorMap tm_v) {
+  extern __shared__ __align__(1024) uint8_t smem_dyn[];
+  uint8_t* smem_raw = smem_dyn + ((1024 - (smem_u32(smem_dyn) & 1023)) & 1023);
+  auto& sm = *reinterpret_cast<BalancedSmem*>(smem_raw);
+  const int warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31;
+  const int B = a.num_seqs;
+  const int Hkv = a.num_kv_heads;
+
+  // ---- blocks per sequence, exclusive prefix in shared memory ------------------
+  if (threadIdx.x == 0) sm.items = 0;
+  __syncthreads();
+  int mine = 0;
+  for (int s = threadIdx.x; s < B; s += kThreads) {
+    int qs, T, ctx;
+    const bool live = sequence_rows<kCausal>(a, s, blockIdx.x == 0, &qs, &T,
+                                             &ctx) &&
+                      T <= a.stream_rows;
+    // a sequence without keys keeps one block, not loaded, for its zero rows
+    sm.pre[s] = live ? max(1, (ctx + kPS - 1) / kPS) : 0;
+    mine += live;
+  }
+  if (mine) atomicAdd(&sm.items, mine);
+  __syncthreads();
+  {
+    const int per = (B + kThreads - 1) / kThreads;
+    const int lo = min(B, (int)threadIdx.x * per);
+    const int hi = min(B, lo + per);
+    int own = 0;
+    for (int s = lo; s < hi; ++s) own += sm.pre[s];
+    int incl = own;
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+      const int v = __shfl_up_sync(0xffffffffu, incl, off);
+      if (lane >= off) incl += v;
+    }
+    if (lane == 31) sm.warp_total[warp] = incl;
+    __syncthreads();
+    int run = incl - own;
+    for (int v = 0; v < warp; ++v) run += sm.warp_total[v];
+    for (int s = lo; s < hi; ++s) {
+      const int n = sm.pre[s];
+      sm.pre[s] = run;
+      run += n;
+    }
+    if (threadIdx.x == kThreads - 1) sm.pre[B] = run;
+  }
+  if (lane == 0) {
+    for (int s = 0; s < kStages; ++s)
+      mbar_init(smem_u32(&sm.ring.full[warp][s]), 1);
+    fence_mbar_init();
+  }
+  __syncthreads();
+
+  // ---- this CTA's range ----------------------------------------------------------
+  const int W = sm.pre[B];
+  const int NG = min((int)gridDim.x / Hkv, max(W / kMinChunkBlocks, sm.items));
+  const int grp = blockIdx.x / Hkv;
+  const int head = blockIdx.x - grp * Hkv;
+  if (grp >= NG) return;
+  auto seq_of = [&](int x) {   // pre[s] <= x < pre[s + 1]
+    int lo = 0, hi = B;
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (sm.pre[mid] <= x) lo = mid; else hi = mid;
+    }
+    return lo;
+  };
+  auto cut = [&](int y) {      // a range boundary, moved to a close sequence end
+    if (y >= W) return W;
+    const int s = seq_of(y);
+    if (y - sm.pre[s] < kSnap) return sm.pre[s];
+    if (sm.pre[s + 1] - y < kSnap) return sm.pre[s + 1];
+    return y;
+  };
+  auto raw_cut = [&](int g) { return (int)((int64_t)g * W / NG); };
+  const int x0 = cut(raw_cut(grp)), x1 = cut(raw_cut(grp + 1));
+  if (x0 >= x1) return;
+
+  // ---- the warp's blocks: x0 + warp + 4 i --------------------------------------------
+  const int my_n =
+      x1 - x0 > warp ? (x1 - x0 - warp + kWarps - 1) / kWarps : 0;
+  auto load_blocks = [&](int batch) -> int {
+    const int i = batch * 32 + lane;
+    if (i >= my_n) return -1;
+    const int x = x0 + warp + kWarps * i;
+    const int s = seq_of(x);
+    // (a sequence without keys reads an entry of its own row, or none)
+    return a.context_lens[s] > 0 ? pool_block(a, s, x - sm.pre[s]) : 0;
+  };
+  const uint64_t policy = l2_policy_evict_first();
+  auto issue = [&](int block, int stage) {
+    issue_block(a, &tm_k, &tm_v, head * kD, block,
+                smem_u32(&sm.ring.slot[warp][stage][0]),
+                smem_u32(&sm.ring.full[warp][stage]), policy);
+  };
+  int cur = load_blocks(0), next = load_blocks(1);
+#pragma unroll
+  for (int j = 0; j < kStages; ++j) {
+    const int block = __shfl_sync(0xffffffffu, cur, j);
+    if (lane == 0 && j < my_n) issue(block, j);
+  }
+  uint32_t koff[4], voff[4];
+  slice_offsets(lane, koff, voff);
+
+  WarpRows<MB, kCausal> rows;
+  bool failed = false;
+  int issued = min(my_n, kStages);
+  int i = 0;                          // blocks this warp has done
+  int seq = seq_of(x0);
+  int next_qs, next_T, next_ctx;
+  sequence_rows<kCausal>(a, seq, false, &next_qs, &next_T, &next_ctx);
+  for (int p0 = x0; p0 < x1;) {
+    const int base = sm.pre[seq];
+    const int end = min(x1, sm.pre[seq + 1]);
+    const int qs = next_qs, T = next_T, ctx = next_ctx;
+    int next_seq = seq;
+    if (end < x1) {   // the next sequence's rows, and its q into the cache
+      do ++next_seq; while (sm.pre[next_seq + 1] <= end);
+      sequence_rows<kCausal>(a, next_seq, false, &next_qs, &next_T, &next_ctx);
+      if (warp == 0 && lane < next_T << a.group_shift)
+        asm volatile("prefetch.global.L1 [%0];" ::"l"(
+            a.q + ((size_t)(next_qs + (lane >> a.group_shift)) *
+                       a.num_q_heads + (head << a.group_shift) +
+                   (lane & ((1 << a.group_shift) - 1))) * kD));
+    }
+    ChunkRows w;
+    w.q_row = qs;
+    w.tb = T;
+    w.first_limit = kCausal ? ctx - T : ctx - 1;
+    w.key_end = ctx;
+    rows.load(a, w, head, lane);
+    rows.clear();
+    for (; i < my_n && !failed; ++i) {
+      const int x = x0 + warp + kWarps * i;
+      if (x >= end) break;
+      const int stage = i % kStages;
+      if ((i & 31) == 0 && i > 0) {
+        cur = next;
+        next = load_blocks((i >> 5) + 1);
+      }
+      const bool page_ok = __shfl_sync(0xffffffffu, cur, i & 31) >= 0;
+      if (!__all_sync(0xffffffffu,
+                      mbar_wait(smem_u32(&sm.ring.full[warp][stage]),
+                                (i / kStages) & 1))) {
+        failed = true;
+        break;
+      }
+      rows.page(&sm.ring.slot[warp][stage][0], (x - base) * kPS, page_ok, w,
+                koff, voff, a.scale_log2, lane);
+      fence_proxy_async_smem();
+      __syncwarp();
+      const int j = i + kStages;
+      const int src = ((j >> 5) == (i >> 5)) ? cur : next;
+      const int block = __shfl_sync(0xffffffffu, src, j & 31);
+      if (j < my_n) {
+        if (lane == 0) issue(block, stage);
+        ++issued;
+      }
+    }
+    if (failed) rows.clear();
+
+    // ---- combine the warps; write, or leave a part ----------------------------------
+    rows.finish_sums();
+    const bool whole = p0 == base && end == sm.pre[seq + 1];
+    const int n_rows = T << a.group_shift;
+    float* part = a.ws_parts + ((size_t)blockIdx.x * 2 + (p0 == x0 ? 0 : 1)) *
+                                   kChunkPartFloats;
+    const int r16 = threadIdx.x >> 3, k8 = threadIdx.x & 7;
+#pragma unroll
+    for (int b = 0; b < MB; ++b) {
+      if (16 * b >= n_rows) break;
+      __syncthreads();   // the last rows have been read
+      rows.put(sm.cb, b, warp, lane);
+      __syncthreads();
+      const int row = 16 * b + r16;
+      if (row >= n_rows) continue;
+      const Joined j = join_warps(sm.cb, r16, k8);
+      if (whole) {
+        j.write(out_row(a, qs, head, row), k8);
+      } else {
+        float4* dst = reinterpret_cast<float4*>(part + 2 * kChunkPartRows +
+                                                row * kD + 4 * k8);
+        __stcg(dst, j.x);
+        __stcg(dst + 8, j.y);
+        if (k8 == 0) {
+          __stcg(part + row, j.M);
+          __stcg(part + kChunkPartRows + row, j.L);
+        }
+      }
+    }
+    if (!whole) {
+      // groups whose boundary lies inside the sequence
+      const int z0 = base + kSnap, z1 = sm.pre[seq + 1] - kSnap;
+      const int g0 = (int)(((int64_t)z0 * NG + W - 1) / W);
+      const int g1 = (int)(((int64_t)(z1 + 1) * NG + W - 1) / W) - 1;
+      const int n_parts = g1 - g0 + 2;
+      __syncthreads();
+      int32_t* counter = a.ws_counters + (size_t)seq * Hkv + head;
+      if (threadIdx.x == 0) {
+        __threadfence();   // the CTA's part, ordered by the barrier
+        sm.last = atomicAdd(counter, 1) == n_parts - 1;
+        __threadfence();
+      }
+      __syncthreads();
+      if (sm.last) {
+        const bool first0 = cut(raw_cut(g0 - 1)) == base;
+        auto part_of = [&](int k) {   // part k is group g0 - 1 + k's
+          return a.ws_parts + ((size_t)((g0 - 1 + k) * Hkv + head) * 2 +
+                               (k == 0 && !first0 ? 1 : 0)) *
+                                  kChunkPartFloats;
+        };
+        for (int row = r16; row < n_rows; row += 16) {
+          Joined j;
+#pragma unroll 4
+          for (int k = 0; k < n_parts; ++k)
+            j.M = fmaxf(j.M, __ldcg(part_of(k) + row));
+#pragma unroll 4
+          for (int k = 0; k < n_parts; ++k) {
+            const float* p = part_of(k);
+            const float4* x = reinterpret_cast<const float4*>(
+                p + 2 * kChunkPartRows + row * kD + 4 * k8);
+            j.add(__ldcg(p + row), __ldcg(p + kChunkPartRows + row),
+                  __ldcg(x), __ldcg(x + 8));
+          }
+          j.write(out_row(a, qs, head, row), k8);
+        }
+        if (threadIdx.x == 0) *counter = 0;
+      }
+    }
+    p0 = end;
+    seq = next_seq;
+  }
+  if (failed) {
+    if (lane == 0) flag_error(a.err, DEVERR_TIMEOUT);
+    for (int k = i; k < issued; ++k)
+      mbar_wait(smem_u32(&sm.ring.full[warp][k % kStages]), (k / kStages) & 1);
+  }
+}
+
+static_assert(3 * (sizeof(BalancedSmem) + 1024 + 1024) <= 228 * 1024,
+              "three CTAs must fit in an SM's shared memory");
+
+template <typename Kernel>
+cudaError_t launch_with(Kernel kern, dim3 grid, int smem, const ChunkArgs& a,
+                        const CUtensorMap& tk, const CUtensorMap& tv,
+                        cudaStream_t stream) {
+  cudaError_t e = cudaFuncSetAttribute(
+      kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e != cudaSuccess) return e;
+  kern<<<grid, kThreads, smem, stream>>>(a, tk, tv);
+  return cudaGetLastError();
 }
 
 template <int MB, bool kCausal>
 cudaError_t launch_mb(const ChunkArgs& a, const CUtensorMap& tk,
                       const CUtensorMap& tv, cudaStream_t stream) {
-  constexpr int kStages = 3;
-  auto kern = paged_chunk_kernel<MB, kStages, kCausal>;
-  const int smem = sizeof(ChunkSmem<MB, kStages>) + 1024;
-  cudaError_t e = cudaFuncSetAttribute(
-      kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-  if (e != cudaSuccess) return e;
+  if (a.balanced_ctas)
+    return launch_with(balanced_chunk_kernel<MB, kCausal>,
+                       dim3(a.balanced_ctas), sizeof(BalancedSmem) + 1024, a,
+                       tk, tv, stream);
   const int per = (16 * MB) >> a.group_shift;
-  dim3 grid(a.num_kv_heads, a.num_seqs, (a.max_query_len + per - 1) / per);
-  kern<<<grid, kThreads, smem, stream>>>(a, tk, tv);
-  return cudaGetLastError();
+  return launch_with(paged_chunk_kernel<MB, kCausal>,
+                     dim3(a.num_kv_heads, a.num_seqs,
+                          (a.max_query_len + per - 1) / per),
+                     sizeof(ChunkRing) + 1024, a, tk, tv, stream);
 }
 
 }  // namespace

@@ -799,7 +799,14 @@ tv_status tv_paged_prefill(void* out, const void* q, int64_t num_query_rows,
 
 // ---- attention of a chunk of rows per sequence -----------------------------------
 
-static size_t chunk_workspace_bytes(int, int, int, int) { return 0; }
+// Workspace: the counters of cut sequences, then the parts of the balanced
+// grid's CTAs.
+static int chunk_ctas() { return device_sms() * tv::kChunkCtasPerSm; }
+
+static size_t chunk_workspace_bytes(int num_seqs, int num_kv_heads) {
+  return counters_bytes(num_seqs, num_kv_heads) +
+         (size_t)chunk_ctas() * 2 * tv::kChunkPartFloats * sizeof(float);
+}
 
 tv_status tv_chunk_workspace_size(int num_seqs, int max_query_len,
                                   int num_q_heads, int num_kv_heads,
@@ -808,8 +815,7 @@ tv_status tv_chunk_workspace_size(int num_seqs, int max_query_len,
       check_attention_shape(num_q_heads, num_kv_heads, head_dim, kPageSize);
   if (st != TV_OK) return st;
   if (!bytes || num_seqs < 0 || max_query_len < 0) return TV_ERR_INVALID_ARG;
-  *bytes = chunk_workspace_bytes(num_seqs, max_query_len, num_q_heads,
-                                 num_kv_heads);
+  *bytes = chunk_workspace_bytes(num_seqs, num_kv_heads);
   return TV_OK;
 }
 
@@ -849,8 +855,7 @@ static tv_status chunk_common(void* out, const void* q, int64_t num_query_rows,
     return TV_ERR_INVALID_ARG;
   if (workspace && (!aligned16(workspace) ||
                     workspace_bytes <
-                        chunk_workspace_bytes(num_seqs, max_query_len,
-                                              num_q_heads, num_kv_heads)))
+                        chunk_workspace_bytes(num_seqs, num_kv_heads)))
     return TV_ERR_INVALID_ARG;
 
   CUtensorMap tk, tvm;
@@ -877,6 +882,17 @@ static tv_status chunk_common(void* out, const void* q, int64_t num_query_rows,
   a.scale_log2 = scale * 1.4426950408889634f;
   a.page_shift = page_shift(page_size);
   a.group_shift = group == 8 ? 3 : group >> 1;
+  // the balanced grid holds every sequence's prefix sum in shared memory and
+  // counts blocks in 32 bits
+  a.stream_rows = tv::kChunkPartRows >> a.group_shift;
+  if (workspace && num_seqs <= tv::kMaxChunkSeqs &&
+      max_query_len <= a.stream_rows && num_kv_heads <= chunk_ctas() &&
+      ((int64_t)num_seqs * max_blocks_per_seq << a.page_shift) <= INT32_MAX) {
+    a.balanced_ctas = chunk_ctas();
+    a.ws_counters = static_cast<int32_t*>(workspace);
+    a.ws_parts = reinterpret_cast<float*>(
+        static_cast<char*>(workspace) + counters_bytes(num_seqs, num_kv_heads));
+  }
   return cuda_status(tv::launch_paged_chunk(
       a, tk, tvm, causal, static_cast<cudaStream_t>(stream)));
 }

@@ -202,7 +202,19 @@ struct ChunkArgs {
   float scale_log2;
   int page_shift;                // page_size = 16 << page_shift
   int group_shift;               // query heads per KV head = 1 << group_shift
+  // With a workspace: CTAs of the balanced grid (0: one CTA per KV head, row
+  // block and sequence), which serves the sequences of up to stream_rows rows.
+  int balanced_ctas;
+  int stream_rows;
+  int32_t* ws_counters;          // [B][Hkv], zero between calls
+  float* ws_parts;               // [balanced_ctas][2][kChunkPartFloats]
 };
+constexpr int kMaxChunkSeqs = 1024;     // prefix sums live in shared memory
+constexpr int kMinChunkBlocks = 16;     // 16-token blocks worth a CTA
+constexpr int kChunkPartRows = 32;      // rows x heads per KV head
+// m, l and the unscaled output of one part
+constexpr int kChunkPartFloats = kChunkPartRows * (2 + 64);
+constexpr int kChunkCtasPerSm = 3;
 
 cudaError_t launch_paged_chunk(const ChunkArgs& a, const CUtensorMap& tk,
                                const CUtensorMap& tv, bool causal,
