@@ -799,14 +799,37 @@ tv_status tv_paged_prefill(void* out, const void* q, int64_t num_query_rows,
 
 // ---- attention of a chunk of rows per sequence -----------------------------------
 
-// Workspace: the counters of cut sequences, then the parts of the balanced
-// grid's CTAs.
+// Workspace: the counters (zero between calls) of sequences and blocks that are
+// cut along their keys, then their parts and the tile kernel's plan.
 static int chunk_ctas() { return device_sms() * tv::kChunkCtasPerSm; }
 
-static size_t chunk_workspace_bytes(int num_seqs, int num_kv_heads) {
-  return counters_bytes(num_seqs, num_kv_heads) +
-         (size_t)chunk_ctas() * 2 * tv::kChunkPartFloats * sizeof(float);
+struct ChunkWorkspace {
+  size_t tile_counters, parts, plan, entries, tile_parts, bytes;
+};
+
+static ChunkWorkspace chunk_workspace(int num_seqs, int max_query_len,
+                                      int num_kv_heads, int group_shift) {
+  auto up = [](size_t n) { return (n + 255) / 256 * 256; };
+  const size_t sms = device_sms();
+  const bool tiles =
+      ((int64_t)max_query_len << group_shift) > tv::kChunkPartRows;
+  ChunkWorkspace w;
+  w.tile_counters = counters_bytes(num_seqs, num_kv_heads);
+  w.parts = w.tile_counters + (tiles ? up(sms * 4 * 2 * sizeof(int32_t)) : 0);
+  w.plan = w.parts + up((size_t)chunk_ctas() * 2 * tv::kChunkPartFloats *
+                        sizeof(float));
+  w.entries = w.plan + (tiles ? 256 : 0);
+  // every block once, and the further parts of those that are cut
+  const size_t n = (size_t)num_seqs *
+                       tv::chunk_tile_blocks(max_query_len, group_shift) +
+                   4 * sms;
+  w.tile_parts = w.entries + (tiles ? up(n * sizeof(tv::ChunkEntry)) : 0);
+  w.bytes = w.tile_parts +
+            (tiles ? sms * 4 * tv::kTilePartFloats * sizeof(float) : 0);
+  return w;
 }
+
+static int group_shift_of(int group) { return group == 8 ? 3 : group >> 1; }
 
 tv_status tv_chunk_workspace_size(int num_seqs, int max_query_len,
                                   int num_q_heads, int num_kv_heads,
@@ -815,7 +838,11 @@ tv_status tv_chunk_workspace_size(int num_seqs, int max_query_len,
       check_attention_shape(num_q_heads, num_kv_heads, head_dim, kPageSize);
   if (st != TV_OK) return st;
   if (!bytes || num_seqs < 0 || max_query_len < 0) return TV_ERR_INVALID_ARG;
-  *bytes = chunk_workspace_bytes(num_seqs, num_kv_heads);
+  const int shift = group_shift_of(num_q_heads / num_kv_heads);
+  if (((int64_t)max_query_len << shift) > 65535ll * 16)
+    return TV_ERR_UNSUPPORTED;
+  if (device_sms() <= 0) return cuda_status(cudaErrorUnknown);
+  *bytes = chunk_workspace(num_seqs, max_query_len, num_kv_heads, shift).bytes;
   return TV_OK;
 }
 
@@ -853,10 +880,13 @@ static tv_status chunk_common(void* out, const void* q, int64_t num_query_rows,
   if (!aligned16(out) || !aligned16(q) || !aligned16(k_pool) ||
       !aligned16(v_pool))
     return TV_ERR_INVALID_ARG;
-  if (workspace && (!aligned16(workspace) ||
-                    workspace_bytes <
-                        chunk_workspace_bytes(num_seqs, num_kv_heads)))
-    return TV_ERR_INVALID_ARG;
+  const int shift = group_shift_of(group);
+  ChunkWorkspace ws{};
+  if (workspace) {
+    ws = chunk_workspace(num_seqs, max_query_len, num_kv_heads, shift);
+    if (!aligned16(workspace) || workspace_bytes < ws.bytes)
+      return TV_ERR_INVALID_ARG;
+  }
 
   CUtensorMap tk, tvm;
   st = pool_tensor_map(&tk, k_pool, num_pages, page_size, num_kv_heads,
@@ -881,17 +911,31 @@ static tv_status chunk_common(void* out, const void* q, int64_t num_query_rows,
   a.num_query_rows = num_query_rows;
   a.scale_log2 = scale * 1.4426950408889634f;
   a.page_shift = page_shift(page_size);
-  a.group_shift = group == 8 ? 3 : group >> 1;
+  a.group_shift = shift;
+  a.stream_rows = tv::kChunkPartRows >> shift;
   // the balanced grid holds every sequence's prefix sum in shared memory and
   // counts blocks in 32 bits
-  a.stream_rows = tv::kChunkPartRows >> a.group_shift;
   if (workspace && num_seqs <= tv::kMaxChunkSeqs &&
-      max_query_len <= a.stream_rows && num_kv_heads <= chunk_ctas() &&
+      num_kv_heads <= chunk_ctas() &&
       ((int64_t)num_seqs * max_blocks_per_seq << a.page_shift) <= INT32_MAX) {
+    char* base = static_cast<char*>(workspace);
     a.balanced_ctas = chunk_ctas();
-    a.ws_counters = static_cast<int32_t*>(workspace);
-    a.ws_parts = reinterpret_cast<float*>(
-        static_cast<char*>(workspace) + counters_bytes(num_seqs, num_kv_heads));
+    a.ws_counters = reinterpret_cast<int32_t*>(base);
+    a.ws_parts = reinterpret_cast<float*>(base + ws.parts);
+    if (max_query_len > a.stream_rows) {
+      a.tile_ctas = device_sms();
+      a.plan = reinterpret_cast<tv::ChunkPlan*>(base + ws.plan);
+      a.plan_entries = reinterpret_cast<tv::ChunkEntry*>(base + ws.entries);
+      a.tile_counters = reinterpret_cast<int32_t*>(base + ws.tile_counters);
+      a.tile_parts = reinterpret_cast<float*>(base + ws.tile_parts);
+      CUtensorMap tq;
+      st = query_tensor_map(&tq, q, num_query_rows, num_q_heads, group,
+                            128 >> shift);
+      if (st != TV_OK) return st;
+      st = cuda_status(tv::launch_chunk_tiles(
+          a, tq, tk, tvm, causal, static_cast<cudaStream_t>(stream)));
+      if (st != TV_OK) return st;
+    }
   }
   return cuda_status(tv::launch_paged_chunk(
       a, tk, tvm, causal, static_cast<cudaStream_t>(stream)));

@@ -184,7 +184,17 @@ cudaError_t launch_paged_prefill(const PrefillArgs& a, const CUtensorMap& tq,
                                  const CUtensorMap& tk, const CUtensorMap& tv,
                                  cudaStream_t stream);
 
-// Attention of a chunk of rows per sequence (paged_chunk.cu).
+// Attention of a chunk of rows per sequence (paged_chunk.cu, and for more than
+// stream_rows rows paged_chunk_tile.cu).
+struct ChunkEntry {              // work of the tile kernel, for every KV head
+  int32_t seq, blk;              // sequence, block of 256 rows x heads
+  int32_t tile0, tile1;          // range of key tiles
+  int32_t part_base, part, parts;  // of a block cut along the keys
+  int32_t pad;
+};
+struct ChunkPlan {
+  int32_t entries;
+};
 struct ChunkArgs {
   __nv_bfloat16* out;            // [rows][Hq][D]
   const __nv_bfloat16* q;        // [rows][Hq][D]
@@ -208,6 +218,12 @@ struct ChunkArgs {
   int stream_rows;
   int32_t* ws_counters;          // [B][Hkv], zero between calls
   float* ws_parts;               // [balanced_ctas][2][kChunkPartFloats]
+  // The tile kernel's part of the workspace (tile_ctas 0: not launched).
+  int tile_ctas;
+  ChunkPlan* plan;
+  ChunkEntry* plan_entries;
+  int32_t* tile_counters;        // [4 tile_ctas][2], zero between calls
+  float* tile_parts;             // [4 tile_ctas][kTilePartFloats]
 };
 constexpr int kMaxChunkSeqs = 1024;     // prefix sums live in shared memory
 constexpr int kMinChunkBlocks = 16;     // 16-token blocks worth a CTA
@@ -215,9 +231,19 @@ constexpr int kChunkPartRows = 32;      // rows x heads per KV head
 // m, l and the unscaled output of one part
 constexpr int kChunkPartFloats = kChunkPartRows * (2 + 64);
 constexpr int kChunkCtasPerSm = 3;
+// m, l and the unscaled output of two query tiles of 128 rows
+constexpr int kTilePartFloats = 2 * 128 * (2 + 64);
+__host__ __device__ inline int chunk_tile_blocks(int max_query_len,
+                                                 int group_shift) {
+  return (int)((((int64_t)max_query_len << group_shift) + 255) / 256);
+}
 
 cudaError_t launch_paged_chunk(const ChunkArgs& a, const CUtensorMap& tk,
                                const CUtensorMap& tv, bool causal,
                                cudaStream_t stream);
+// The plan kernel and the tile kernel.
+cudaError_t launch_chunk_tiles(const ChunkArgs& a, const CUtensorMap& tq,
+                               const CUtensorMap& tk, const CUtensorMap& tv,
+                               bool causal, cudaStream_t stream);
 
 }  // namespace tv
