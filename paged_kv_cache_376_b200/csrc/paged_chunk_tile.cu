@@ -17,19 +17,23 @@
 //  * A plan kernel (one CTA) lists the work: (sequence, block of 256 rows),
 //    cut along the keys where one block would hold an SM for more than half
 //    of an SM's share, costliest first.  A resident grid of one CTA per SM
-//    takes (entry, KV head) units from it in a fixed order, back and forth,
-//    so the shares come out even and no CTA starts a long unit last.
-//  * A CTA owns two 128-row query tiles (A, B) that share every K/V tile; the
-//    tensor core works for one while the other's softmax runs.
-//  * S and P have tensor-memory columns of their own: the softmax copies S
-//    into registers at once and hands the columns back, so S of the next
-//    key tile is computed during the exponentials of this one.  P never
-//    goes through shared memory: P.V reads it from tensor memory.
+//    takes (entry, KV head) units from it, the next one fetched while the
+//    last one loads, so no SM starts a long unit when the others end.
+//  * A CTA owns two 128-row query tiles that share every K/V tile of 128 keys;
+//    the tensor core works for one while the other's softmax runs.
+//  * A key tile is two halves of 64 keys.  P of a half takes the tensor-memory
+//    columns of its S (P.V reads it from there, never through shared memory),
+//    and a query tile has three such buffers: while one is exponentiated, S of
+//    the next two is being computed or has been, and P.V of the last runs.
 //  * warp 0 loads (K/V ring of 4 tiles of 128 keys, 16 page boxes each; q,
 //    double buffered, so the next unit's loads run ahead); warp 3 issues
-//    S = Q K^T for both tiles, warps 1 / 2 issue O += P V of tile A / B
-//    (three issuing threads, because issuing takes longer than the products);
-//    warps 4-7 / 8-11 are the softmax of tile A / B, one row per thread.
+//    S = Q K^T, warps 1 / 2 issue O += P V of query tile 0 / 1 (three issuing
+//    threads, because issuing takes longer than the products); warps 4-7 /
+//    8-11 are the softmax of query tile 0 / 1, one row per thread.
+//  * The softmax exponentiates against its offset as it stands and takes the
+//    maximum beside it; only where a row's maximum grew by more than 2^8 (and
+//    at a unit's first half) does it move the offset, rescale O and the sum
+//    and exponentiate again from the registers.
 //  * P enters the second product in bf16.  A weight's rounding (2^-9 of it)
 //    averages out over the keys of a row, except where there are few: units
 //    whose first row sees fewer than kExactKeys keys add P's remainder,
@@ -51,6 +55,7 @@ constexpr int kD = 64;
 constexpr int kPS = 16;
 constexpr int kBM = 128;                  // rows of a query tile
 constexpr int kBN = 128;                  // keys of a key tile
+constexpr int kHalf = 64;                 // keys of a half tile
 constexpr int kST = 4;                    // K/V ring depth
 constexpr int kPages = kBN / kPS;         // 16-token boxes of a key tile
 constexpr int kRowBytes = kD * 2;
@@ -58,14 +63,15 @@ constexpr int kTileBytes = kBN * kRowBytes;
 constexpr int kPageBytes = kPS * kRowBytes;
 constexpr int kThreads = 384;
 constexpr int kTmemCols = 512;
-constexpr int kSCol = 0;                  // S of tile t: [128 t, +128)
-constexpr int kPCol = 256;                // P of tile t: [256 + 64 t, +64)
+constexpr int kBuf = 3;                   // S/P buffers of a query tile
+constexpr int kSCol = 0;                  // S, then P, in buffer b of query
+                                          // tile t: [64 (3 t + b), +64)
 constexpr int kOCol = 384;                // O of tile t: [384 + 64 t, +64)
 constexpr float kLazy = 8.f;              // log2 of the growth allowed
 constexpr int kExactKeys = 512;           // see the file comment
 constexpr int kMinTiles = 4;              // key tiles worth a unit of their own
 
-constexpr uint32_t kIdescQK = idesc_bf16_f32(kBM, kBN, false);
+constexpr uint32_t kIdescQK = idesc_bf16_f32(kBM, kHalf, false);
 constexpr uint32_t kIdescPV = idesc_bf16_f32(kBM, kD, true);
 
 // ---- plan -----------------------------------------------------------------------
@@ -136,14 +142,18 @@ __global__ void __launch_bounds__(kPlanThreads, 1)
   auto cuts_of = [&](int n) {
     return n > longest ? (int)((n + longest - 1) / longest) : 1;
   };
+  // key tiles, two thirds of them where there is one query tile
+  const int per = kBM >> a.group_shift;
+  auto cost = [&](const Block& b, int n) {
+    return min(b.tb > per ? 3 * n : 2 * n, kBuckets - 1);
+  };
   auto edge = [](int n, int k, int of) { return (int)((long long)n * k / of); };
   for (int i = threadIdx.x; i < n_items; i += kPlanThreads) {
     const int n = tiles_of(i, &b);
     if (n < 0) continue;
     const int of = cuts_of(n);
     for (int k = 0; k < of; ++k)
-      atomicAdd(&slot[min(edge(n, k + 1, of) - edge(n, k, of), kBuckets - 1)],
-                1);
+      atomicAdd(&slot[cost(b, edge(n, k + 1, of) - edge(n, k, of))], 1);
   }
   __syncthreads();
   // thread t owns the costs kBuckets-1-4t down to ...-4t-3
@@ -179,7 +189,10 @@ __global__ void __launch_bounds__(kPlanThreads, 1)
     slot[kBuckets - 1 - (threadIdx.x * kPerThread + k)] = start;
     start += own[k];
   }
-  if (threadIdx.x == kPlanThreads - 1) a.plan->entries = start;
+  if (threadIdx.x == kPlanThreads - 1) {
+    a.plan->entries = start;
+    a.plan->next = a.tile_ctas;
+  }
   __syncthreads();
   for (int i = threadIdx.x; i < n_items; i += kPlanThreads) {
     const int n = tiles_of(i, &b);
@@ -197,59 +210,12 @@ __global__ void __launch_bounds__(kPlanThreads, 1)
       e.part = k;
       e.parts = of;
       e.pad = 0;
-      a.plan_entries[atomicAdd(&slot[min(k1 - k0, kBuckets - 1)], 1)] = e;
+      a.plan_entries[atomicAdd(&slot[cost(b, k1 - k0)], 1)] = e;
     }
   }
 }
 
-// ---- tensor memory ------------------------------------------------------------------
-// 128 consecutive columns of the warp's 32 lanes, one lane per thread; the
-// wait sits in the same statement, so no use can be scheduled before it.
-#define TV_R8(r, i) "=r"(r[i]), "=r"(r[i + 1]), "=r"(r[i + 2]), \
-    "=r"(r[i + 3]), "=r"(r[i + 4]), "=r"(r[i + 5]), "=r"(r[i + 6]), \
-    "=r"(r[i + 7])
-__device__ __forceinline__ void tmem_ld128(uint32_t taddr, float (&v)[128]) {
-  uint32_t r[128];
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x128.b32 "
-      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
-      "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, "
-      "%30, %31, %32, %33, %34, %35, %36, %37, %38, %39, %40, %41, %42, %43, "
-      "%44, %45, %46, %47, %48, %49, %50, %51, %52, %53, %54, %55, %56, %57, "
-      "%58, %59, %60, %61, %62, %63, %64, %65, %66, %67, %68, %69, %70, %71, "
-      "%72, %73, %74, %75, %76, %77, %78, %79, %80, %81, %82, %83, %84, %85, "
-      "%86, %87, %88, %89, %90, %91, %92, %93, %94, %95, %96, %97, %98, %99, "
-      "%100, %101, %102, %103, %104, %105, %106, %107, %108, %109, %110, "
-      "%111, %112, %113, %114, %115, %116, %117, %118, %119, %120, %121, "
-      "%122, %123, %124, %125, %126, %127}, [%128];\n\t"
-      "tcgen05.wait::ld.sync.aligned;"
-      : TV_R8(r, 0), TV_R8(r, 8), TV_R8(r, 16), TV_R8(r, 24), TV_R8(r, 32),
-        TV_R8(r, 40), TV_R8(r, 48), TV_R8(r, 56), TV_R8(r, 64), TV_R8(r, 72),
-        TV_R8(r, 80), TV_R8(r, 88), TV_R8(r, 96), TV_R8(r, 104),
-        TV_R8(r, 112), TV_R8(r, 120)
-      : "r"(taddr)
-      : "memory");
-#pragma unroll
-  for (int i = 0; i < 128; ++i) v[i] = __uint_as_float(r[i]);
-}
-
 // ---- the kernel ------------------------------------------------------------------------
-struct TileSmem {
-  alignas(1024) uint8_t q[2][2][kBM * kRowBytes];   // [unit parity][tile]
-  alignas(1024) uint8_t k[kST][kTileBytes];
-  alignas(1024) uint8_t v[kST][kTileBytes];
-  alignas(8) uint64_t q_full[2];
-  uint64_t q_empty[2];       // S issued and the unit's results written
-  uint64_t kv_full[kST], kv_empty[kST];
-  uint64_t v_ready[kST];     // V of an edge tile is clean
-  uint64_t s_full[2], s_free[2], p_full[2], o_done[2], o_free[2];
-  uint64_t drain[3];
-  uint32_t tmem_base;
-  uint32_t bad_pages[kST];
-  int32_t poison[2][kD];     // [unit parity]: first key with a non-finite V
-  int32_t last[2];
-};
-
 // A unit: a plan entry for one KV head, and what follows from it.
 struct Unit {
   ChunkEntry e;
@@ -258,16 +224,49 @@ struct Unit {
   int n[2];        // key tiles of query tile 0 / 1, from e.tile0 on
   int n_tiles;     // key tiles loaded
   int edge0;       // first key tile with a key that some row does not see
+  int live;        // 0: no more units
+};
+
+struct TileSmem {
+  alignas(1024) uint8_t q[2][2][kBM * kRowBytes];   // [unit parity][tile]
+  alignas(1024) uint8_t k[kST][kTileBytes];
+  alignas(1024) uint8_t v[kST][kTileBytes];
+  alignas(8) uint64_t q_full[2];
+  uint64_t q_empty[2];       // every other warp is done with the unit
+  uint64_t unit_full[2];     // the unit is in `unit`
+  uint64_t kv_full[kST], kv_empty[kST];
+  uint64_t v_ready[kST];     // V of an edge tile is clean
+  uint64_t s_full[2][kBuf], p_full[2][kBuf], o_done[2][kBuf];
+  uint64_t o_free[2], part_in[2], part_out[2];     // [query tile]
+  uint64_t drain[3];
+  uint32_t tmem_base;
+  uint32_t bad_pages[kST];
+  uint64_t clean[2];         // [unit parity]: `poison` is complete
+  int32_t poison[2][kD];     // first key with a non-finite V
+  int32_t poisoned[2];       // any of them
+  int32_t bad_unit[2];       // a page of the unit so far was bad
+  int32_t last[2];
+  Unit unit[2];              // [unit parity]
+};
+
+// The S/P buffer of a half and the parity of this use of its barriers.
+struct Turn {
+  int b = 0;
+  uint32_t parity = 0;
+  __device__ __forceinline__ void next() {
+    if (++b == kBuf) {
+      b = 0;
+      parity ^= 1;
+    }
+  }
 };
 
 template <bool kCausal>
-__device__ __forceinline__ bool unit_at(const ChunkArgs& a, int round,
-                                        int n_units, Unit* u) {
-  // back and forth over the sorted list
-  const int g = gridDim.x;
-  const int i = round * g + ((round & 1) ? g - 1 - (int)blockIdx.x
-                                         : (int)blockIdx.x);
-  if (i >= n_units) return false;
+__device__ __forceinline__ void unit_at(const ChunkArgs& a, int i, int n_units,
+                                        Unit* u) {
+  u->live = i < n_units;
+  u->n_tiles = 0;
+  if (!u->live) return;
   u->e = a.plan_entries[i / a.num_kv_heads];
   u->kvh = i % a.num_kv_heads;
   tile_block<kCausal>(a, u->e.seq, u->e.blk, &u->b);
@@ -282,11 +281,115 @@ __device__ __forceinline__ bool unit_at(const ChunkArgs& a, int round,
   }
   u->n_tiles = u->e.tile1 - u->e.tile0;
   u->edge0 = max(0, u->b.first_limit + 1) / kBN;
-  return true;
+}
+
+// One thread of a converged warp; the compiler knows that there is one, and
+// feeds the products' descriptors through uniform registers (the issue of four
+// of them takes 194 clocks, under `lane == 0` 250; the tensor core needs 184).
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(p));
+  return p != 0;
+}
+// Four products over 64 elements of K.  S = Q K^T: both operands K-major, 32
+// bytes on per 16 elements.
+__device__ __forceinline__ void issue_qk(uint32_t d, uint32_t q, uint32_t k,
+                                         uint32_t desc_hi, uint32_t bar) {
+#pragma unroll
+  for (int i = 0; i < kD / 16; ++i)
+    tc_mma_bf16(d, (uint64_t)desc_hi << 32 | (q + 2 * i),
+                (uint64_t)desc_hi << 32 | (k + 2 * i), kIdescQK, i > 0);
+  tc_commit(bar);
+}
+// O += P V: 16 keys are 8 columns of P, and 2 x 8 rows of V (MN-major).
+__device__ __forceinline__ void issue_pv(uint32_t d, uint32_t p, uint32_t v,
+                                         uint32_t desc_hi, bool accumulate) {
+#pragma unroll
+  for (int i = 0; i < kHalf / 16; ++i)
+    tc_mma_bf16_ts(d, p + 8 * i,
+                   (uint64_t)desc_hi << 32 | (v + (2 * i * 1024 >> 4)),
+                   kIdescPV, accumulate || i > 0);
 }
 
 __device__ __forceinline__ bool wait_warp(uint64_t* bar, uint32_t parity) {
   return __all_sync(0xffffffffu, mbar_wait(smem_u32(bar), parity));
+}
+
+// 32 columns of the warp's 32 lanes, one lane per thread; the registers hold
+// them after tmem_wait32 (through which they are passed, so that no use is
+// scheduled before it).
+#define TV_OUT8(r, i)                                                     \
+  "=r"(r[i]), "=r"(r[i + 1]), "=r"(r[i + 2]), "=r"(r[i + 3]),             \
+      "=r"(r[i + 4]), "=r"(r[i + 5]), "=r"(r[i + 6]), "=r"(r[i + 7])
+#define TV_INOUT8(r, i)                                                   \
+  "+r"(r[i]), "+r"(r[i + 1]), "+r"(r[i + 2]), "+r"(r[i + 3]),             \
+      "+r"(r[i + 4]), "+r"(r[i + 5]), "+r"(r[i + 6]), "+r"(r[i + 7])
+__device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t (&r)[32]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+      "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, "
+      "%30, %31}, [%32];"
+      : TV_OUT8(r, 0), TV_OUT8(r, 8), TV_OUT8(r, 16), TV_OUT8(r, 24)
+      : "r"(taddr)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_wait32(uint32_t (&r)[32]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : TV_INOUT8(r, 0), TV_INOUT8(r, 8), TV_INOUT8(r, 16),
+                 TV_INOUT8(r, 24)
+               :
+               : "memory");
+}
+
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, "
+      "[%16];\n\ttcgen05.wait::ld.sync.aligned;"
+      : TV_OUT8(r, 0), TV_OUT8(r, 8)
+      : "r"(taddr)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_st16(uint32_t taddr,
+                                          const uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, "
+      "%7, %8, %9, %10, %11, %12, %13, %14, %15, %16};\n\t"
+      "tcgen05.wait::st.sync.aligned;" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]),
+      "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]),
+      "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      : "memory");
+}
+
+// 2^x of a pair on the FMA units: x = n + f, |f| <= 1/2 (n by adding and
+// subtracting 1.5 x 2^23), 2^f by the cubic of least relative error on that
+// range (Remez exchange; 7.5e-5, against the 2^-9 of the bf16 that it becomes),
+// 2^n from its exponent bits.  Below 2^-126 it stays there.
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ float2 exp2_cubic(float2 x) {
+  const float2 big = make_float2(12582912.f, 12582912.f);
+  const float2 nbig = make_float2(-12582912.f, -12582912.f);
+  x = make_float2(max_nan(x.x, -126.f), max_nan(x.y, -126.f));
+  const float2 t = __fadd2_rn(x, big);
+  const float2 n = __fadd2_rn(t, nbig);
+  const float2 f = __ffma2_rn(n, make_float2(-1.f, -1.f), x);
+  float2 p = __ffma2_rn(make_float2(0.0551716685f, 0.0551716685f), f,
+                        make_float2(0.242611125f, 0.242611125f));
+  p = __ffma2_rn(p, f, make_float2(0.693260968f, 0.693260968f));
+  p = __ffma2_rn(p, f, make_float2(0.999928057f, 0.999928057f));
+  const float2 scale =
+      make_float2(__int_as_float((__float_as_int(t.x) << 23) + 0x3f800000),
+                  __int_as_float((__float_as_int(t.y) << 23) + 0x3f800000));
+  return __fmul2_rn(p, scale);   // NaN x stays NaN
 }
 
 // Rows [r0, 128) of a V tile that holds the keys key0 .. : rows behind the last
@@ -294,7 +397,7 @@ __device__ __forceinline__ bool wait_warp(uint64_t* bar, uint32_t parity) {
 // their key went into `poison` (all by one warp).
 __device__ __forceinline__ void clean_v(uint8_t* v, int key0, int r0,
                                         int key_end, int32_t* poison,
-                                        int lane) {
+                                        int32_t* poisoned, int lane) {
   for (int i = r0 * 8 + lane; i < kBN * 8; i += 32) {
     const int r = i >> 3;
     uint4* p = reinterpret_cast<uint4*>(v + i * 16);
@@ -310,6 +413,7 @@ __device__ __forceinline__ void clean_v(uint8_t* v, int key0, int r0,
       any |= (w[k] & 0x7f80u) == 0x7f80u ||
              (w[k] & 0x7f800000u) == 0x7f800000u;
     if (!any) continue;
+    *poisoned = 1;
     const int d0 = ((i & 7) ^ (r & 7)) * 8;     // the slice is swizzled
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
@@ -344,12 +448,17 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (threadIdx.x == 0) {
     for (int i = 0; i < 2; ++i) {
       mbar_init(smem_u32(&sm.q_full[i]), 1);
-      mbar_init(smem_u32(&sm.q_empty[i]), 1 + 8);
-      mbar_init(smem_u32(&sm.s_full[i]), 1);
-      mbar_init(smem_u32(&sm.s_free[i]), 4);
-      mbar_init(smem_u32(&sm.p_full[i]), 4);
-      mbar_init(smem_u32(&sm.o_done[i]), 1);
+      mbar_init(smem_u32(&sm.q_empty[i]), 3 + 8);
+      mbar_init(smem_u32(&sm.unit_full[i]), 1);
+      mbar_init(smem_u32(&sm.clean[i]), 1);
       mbar_init(smem_u32(&sm.o_free[i]), 4);
+      for (int k = 0; k < kBuf; ++k) {
+        mbar_init(smem_u32(&sm.s_full[i][k]), 1);
+        mbar_init(smem_u32(&sm.p_full[i][k]), 4);
+        mbar_init(smem_u32(&sm.o_done[i][k]), 1);
+      }
+      mbar_init(smem_u32(&sm.part_in[i]), 4);
+      mbar_init(smem_u32(&sm.part_out[i]), 1);
     }
     for (int i = 0; i < kST; ++i) {
       mbar_init(smem_u32(&sm.kv_full[i]), 1);
@@ -368,15 +477,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_after();
   const uint32_t tmem = sm.tmem_base;
 
-  // Counters that run through all units of the CTA: `it` K/V tiles, `c` tile
-  // passes of a query tile.  A barrier's n-th use (from 0) completes its phase
-  // of parity n & 1.
-  Unit u;
-  if (warp < 4) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
-  } else {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
-  }
+  // `it` counts the K/V tiles of all units of the CTA, a Turn the halves of a
+  // query tile.  A barrier's n-th use (from 0) completes its phase of parity
+  // n & 1.
   if (warp == 0) {
     // ======================= loads =============================================
     const int oob_row = (a.num_pages << a.page_shift) * kPS;   // reads as zeros
@@ -384,14 +487,25 @@ __global__ void __launch_bounds__(kThreads, 1)
     const bool is_v = lane & 1;
     const CUtensorMap* tmap = is_v ? &tm_v : &tm_k;
     bool ok = true;
-    uint32_t it = 0, v_uses = 0;
-    for (int round = 0; ok && unit_at<kCausal>(a, round, n_units, &u);
-         ++round) {
+    uint32_t it = 0;
+    int unit = blockIdx.x;
+    for (int round = 0;; ++round) {
       const int ub = round & 1;
       if (round >= 2 && !wait_warp(&sm.q_empty[ub], ((round >> 1) - 1) & 1)) {
         ok = false;
         break;
       }
+      Unit u;
+      unit_at<kCausal>(a, unit, n_units, &u);
+      if (lane == 0) {
+        sm.unit[ub] = u;
+        sm.poisoned[ub] = 0;
+        sm.bad_unit[ub] = 0;
+        mbar_arrive(smem_u32(&sm.unit_full[ub]));
+      }
+      if (!u.live) break;
+      // the number after this one, fetched while this unit loads
+      if (lane == 0) unit = atomicAdd(&a.plan->next, 1);
       sm.poison[ub][lane] = sm.poison[ub][lane + 32] = INT32_MAX;
       if (lane == 0) {
         const uint32_t qbar = smem_u32(&sm.q_full[ub]);
@@ -405,30 +519,39 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int32_t* bt =
           a.block_tables + (size_t)u.e.seq * a.max_blocks_per_seq;
       const uint32_t it0 = it;
+      // first pool row of the pages of tiles j .. j + 3, one per lane: behind
+      // the last page where a box reads zeros, -1 for a bad page
+      auto page_rows = [&](int j) {
+        const int lp = (u.e.tile0 + j) * kPages + lane;
+        if (lp >= n_pages) return oob_row;
+        const int pid = __ldg(bt + (lp >> a.page_shift));
+        return pid >= 0 && pid < a.num_pages
+                   ? ((pid << a.page_shift) +
+                      (lp & ((1 << a.page_shift) - 1))) * kPS
+                   : -1;
+      };
+      int rows = page_rows(0), rows_ahead = page_rows(4);
       for (int j = 0; j < u.n_tiles; ++j, ++it) {
         const int st = it % kST;
         if (it >= kST && !wait_warp(&sm.kv_empty[st], (it / kST + 1) & 1)) {
           ok = false;
           break;
         }
-        int y = oob_row;
-        bool badp = false;
-        if (lane < kPages) {       // lane p looks up page p of the tile
-          const int lp = (u.e.tile0 + j) * kPages + lane;
-          if (lp < n_pages) {
-            const int pid = __ldg(bt + (lp >> a.page_shift));
-            if (pid >= 0 && pid < a.num_pages)
-              y = ((pid << a.page_shift) + (lp & ((1 << a.page_shift) - 1))) *
-                  kPS;
-            else
-              badp = true;
-          }
+        if ((j & 3) == 0 && j > 0) {   // the next four tiles' pages
+          rows = rows_ahead;
+          rows_ahead = page_rows(j + 4);
         }
-        const uint32_t bad = __ballot_sync(0xffffffffu, badp);
-        const int row = __shfl_sync(0xffffffffu, y, pp);
+        const int src = (j & 3) * kPages;
+        const int y = __shfl_sync(0xffffffffu, rows, src + pp);
+        const uint32_t bad =
+            (__ballot_sync(0xffffffffu, rows < 0) >> src) & 0xffu;
+        const int row = y < 0 ? oob_row : y;
         const uint32_t bar = smem_u32(&sm.kv_full[st]);
         if (lane == 0) {
-          if (bad) flag_error(a.err, DEVERR_BAD_PAGE);
+          if (bad) {
+            flag_error(a.err, DEVERR_BAD_PAGE);
+            sm.bad_unit[ub] = 1;
+          }
           sm.bad_pages[st] = bad;
           mbar_arrive_expect_tx(bar, 2 * kTileBytes);
         }
@@ -447,12 +570,14 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         const int key0 = (u.e.tile0 + j) * kBN;
         clean_v(sm.v[st], key0, max(0, u.b.first_limit + 1 - key0),
-                u.b.key_end, sm.poison[ub], lane);
+                u.b.key_end, sm.poison[ub], &sm.poisoned[ub], lane);
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(smem_u32(&sm.v_ready[st]));
-        v_uses ^= 1u << st;
       }
+      if (!ok) break;
+      if (lane == 0) mbar_arrive(smem_u32(&sm.clean[ub]));
+      unit = __shfl_sync(0xffffffffu, unit, 0);
     }
     if (!ok && lane == 0) flag_error(a.err, DEVERR_TIMEOUT);
     // no copy may be in flight when the CTA ends (bounded waits; all of them
@@ -462,97 +587,123 @@ __global__ void __launch_bounds__(kThreads, 1)
         mbar_wait(smem_u32(&sm.kv_full[i % kST]), (i / kST) & 1);
   } else if (warp < 4) {
     // ======================= MMA issuers =======================================
-    if (lane == 0) {
-      bool ok = true;
-      uint32_t it = 0, v_uses = 0;
-      uint32_t c[2] = {0, 0};
-      for (int round = 0; ok && unit_at<kCausal>(a, round, n_units, &u);
-           ++round) {
-        if (warp == 3) {
-          const int ub = round & 1;
-          ok = mbar_wait(smem_u32(&sm.q_full[ub]), (round >> 1) & 1);
-          for (int j = 0; ok && j < u.n_tiles; ++j, ++it) {
-            const int st = it % kST;
-            if (!mbar_wait(smem_u32(&sm.kv_full[st]), (it / kST) & 1)) {
-              ok = false;
-              break;
-            }
+    const bool leader = elect_one();
+    // shared-memory descriptors: address >> 4 in the low word, strides and
+    // layout in the high one (V: see smem_desc_sw128's leading offset)
+    const uint64_t dq = smem_desc_sw128(smem_u32(sm.q[0][0]), 16, 1024);
+    const uint64_t dk = smem_desc_sw128(smem_u32(sm.k[0]), 16, 1024);
+    const uint64_t dv = smem_desc_sw128(smem_u32(sm.v[0]), kTileBytes, 1024);
+    const uint32_t hi_k = (uint32_t)(dk >> 32), hi_v = (uint32_t)(dv >> 32);
+    bool ok = true;
+    uint32_t it = 0, v_uses = 0;
+    Turn turn[2];
+    uint32_t results = 0;
+    for (int round = 0;; ++round) {
+      const int ub = round & 1;
+      ok = wait_warp(&sm.unit_full[ub], (round >> 1) & 1);
+      if (!ok || !sm.unit[ub].live) break;
+      const Unit& u = sm.unit[ub];
+      const int n_tiles = u.n_tiles;
+      if (warp == 3) {
+        const int n0 = u.n[0], n1 = u.n[1];
+        ok = wait_warp(&sm.q_full[ub], (round >> 1) & 1);
+        const uint32_t q_lo = (uint32_t)dq + ub * (2 * kBM * kRowBytes >> 4);
+        for (int j = 0; ok && j < n_tiles; ++j, ++it) {
+          const int st = it % kST;
+          if (!wait_warp(&sm.kv_full[st], (it / kST) & 1)) {
+            ok = false;
+            break;
+          }
+          const uint32_t k_lo = (uint32_t)dk + st * (kTileBytes >> 4);
+#pragma unroll
+          for (int half = 0; half < 2; ++half)
 #pragma unroll
             for (int t = 0; t < 2; ++t) {
-              if (j >= u.n[t]) continue;
-              // the softmax has taken the last S out of the columns
-              if (c[t] > 0 &&
-                  !mbar_wait(smem_u32(&sm.s_free[t]), (c[t] - 1) & 1)) {
+              if (!ok || j >= (t ? n1 : n0)) continue;
+              Turn& h = turn[t];
+              // P.V of the buffer's last half has read it (true at first)
+              if (!wait_warp(&sm.o_done[t][h.b], h.parity ^ 1)) {
                 ok = false;
-                break;
+                continue;
               }
               tc_fence_after();
-              const uint32_t q_addr = smem_u32(sm.q[ub][t]);
-              const uint32_t k_addr = smem_u32(sm.k[st]);
-#pragma unroll
-              for (int k = 0; k < kD / 16; ++k)
-                tc_mma_bf16(tmem + kSCol + t * kBN,
-                            smem_desc_sw128(q_addr + k * 32, 16, 1024),
-                            smem_desc_sw128(k_addr + k * 32, 16, 1024),
-                            kIdescQK, k > 0);
-              tc_commit(smem_u32(&sm.s_full[t]));
-              ++c[t];
+              if (leader)
+                issue_qk(tmem + kSCol + (t * kBuf + h.b) * kHalf,
+                         q_lo + t * (kBM * kRowBytes >> 4),
+                         k_lo + half * (kHalf * kRowBytes >> 4), hi_k,
+                         smem_u32(&sm.s_full[t][h.b]));
+              __syncwarp();
+              h.next();
             }
-            if (!ok) break;
-            tc_commit(smem_u32(&sm.kv_empty[st]));
+          if (!ok) break;
+          if (leader) tc_commit(smem_u32(&sm.kv_empty[st]));
+          __syncwarp();
+        }
+        if (!ok) break;
+        if (leader) tc_commit(smem_u32(&sm.q_empty[ub]));
+        __syncwarp();
+      } else {
+        const int t = warp - 1;
+        Turn& h = turn[0];
+        const int n = u.n[t];
+        const int edge = u.edge0 - u.e.tile0;
+        const int parts = u.b.first_limit + 1 < kExactKeys ? 2 : 1;
+        if (n > 0 && results > 0)   // the last unit's O has been read
+          ok = wait_warp(&sm.o_free[t], (results - 1) & 1);
+        for (int j = 0; ok && j < n_tiles; ++j, ++it) {
+          const int st = it % kST;
+          if (!wait_warp(&sm.kv_full[st], (it / kST) & 1)) {
+            ok = false;
+            break;
           }
-          if (ok) tc_commit(smem_u32(&sm.q_empty[ub]));
-        } else {
-          const int t = warp - 1;
-          const int passes = u.b.first_limit + 1 < kExactKeys ? 2 : 1;
-          if (u.n[t] > 0 && round > 0)   // the last unit's O has been read
-            ok = mbar_wait(smem_u32(&sm.o_free[t]), (c[1] - 1) & 1);
-          for (int j = 0; ok && j < u.n_tiles; ++j, ++it) {
-            const int st = it % kST;
-            if (!mbar_wait(smem_u32(&sm.kv_full[st]), (it / kST) & 1)) {
+          if (j >= edge) {
+            if (!wait_warp(&sm.v_ready[st], (v_uses >> st) & 1)) {
               ok = false;
               break;
             }
-            if (u.e.tile0 + j >= u.edge0) {
-              if (!mbar_wait(smem_u32(&sm.v_ready[st]), (v_uses >> st) & 1)) {
-                ok = false;
-                break;
-              }
-              v_uses ^= 1u << st;
-            }
-            if (j < u.n[t]) {
-              const uint32_t v_addr = smem_u32(sm.v[st]);
-              for (int p = 0; p < passes; ++p, ++c[0]) {
-                if (!mbar_wait(smem_u32(&sm.p_full[t]), c[0] & 1)) {
-                  ok = false;
-                  break;
-                }
-                tc_fence_after();
-#pragma unroll
-                for (int k = 0; k < kBN / 16; ++k)
-                  // A = P: 16 keys are 8 columns; B = V, MN-major (head dim
-                  // contiguous): 16 keys = 2 x 8 rows
-                  tc_mma_bf16_ts(tmem + kOCol + t * kD,
-                                 tmem + kPCol + t * (kBN / 2) + k * 8,
-                                 smem_desc_sw128(v_addr + k * 16 * kRowBytes,
-                                                 kTileBytes, 1024),
-                                 kIdescPV, (j | p | k) != 0);
-                tc_commit(smem_u32(&sm.o_done[t]));
-              }
-              if (!ok) break;
-              tc_commit(smem_u32(&sm.kv_empty[st]));
-            } else {
-              mbar_arrive(smem_u32(&sm.kv_empty[st]));
-            }
+            v_uses ^= 1u << st;
           }
-          if (u.n[t] > 0) ++c[1];        // units with an O of this tile
+          if (j >= n) {
+            if (leader) mbar_arrive(smem_u32(&sm.kv_empty[st]));
+            __syncwarp();
+            continue;
+          }
+          const uint32_t v_lo = (uint32_t)dv + st * (kTileBytes >> 4);
+#pragma unroll
+          for (int half = 0; half < 2; ++half) {
+            if (!ok || !wait_warp(&sm.p_full[t][h.b], h.parity)) {
+              ok = false;
+              continue;
+            }
+            tc_fence_after();
+            if (leader) {
+              const uint32_t p_col = tmem + kSCol + (t * kBuf + h.b) * kHalf;
+              const uint32_t v_half = v_lo + half * (kHalf * kRowBytes >> 4);
+              issue_pv(tmem + kOCol + t * kD, p_col, v_half, hi_v,
+                       (j | half) != 0);
+              if (parts == 2)
+                issue_pv(tmem + kOCol + t * kD, p_col + kHalf / 2, v_half,
+                         hi_v, true);
+              tc_commit(smem_u32(&sm.o_done[t][h.b]));
+            }
+            __syncwarp();
+            h.next();
+          }
+          if (!ok) break;
+          if (leader) tc_commit(smem_u32(&sm.kv_empty[st]));
+          __syncwarp();
         }
+        if (!ok) break;
+        results += n > 0;
+        if (leader) mbar_arrive(smem_u32(&sm.q_empty[ub]));
+        __syncwarp();
       }
-      if (!ok) flag_error(a.err, DEVERR_TIMEOUT);
-      // this thread's products finish before tensor memory is freed
-      tc_commit(smem_u32(&sm.drain[warp - 1]));
-      mbar_wait(smem_u32(&sm.drain[warp - 1]), 0);
     }
+    if (!ok && lane == 0) flag_error(a.err, DEVERR_TIMEOUT);
+    // this thread's products finish before tensor memory is freed
+    if (leader) tc_commit(smem_u32(&sm.drain[warp - 1]));
+    __syncwarp();
+    mbar_wait(smem_u32(&sm.drain[warp - 1]), 0);
   } else {
     // ======================= softmax ===========================================
     const int t = (warp >> 2) - 1;           // query tile
@@ -561,213 +712,283 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int qi = r >> a.group_shift;       // query row of the tile
     const int hh = r & ((1 << a.group_shift) - 1);
     const uint32_t lane_base = (uint32_t)(quarter * 32) << 16;
-    const uint32_t s_addr = tmem + lane_base + kSCol + t * kBN;
-    const uint32_t p_addr = tmem + lane_base + kPCol + t * (kBN / 2);
+    const uint32_t s_addr = tmem + lane_base + kSCol + t * kBuf * kHalf;
     const uint32_t o_addr = tmem + lane_base + kOCol + t * kD;
     const float cs = a.scale_log2;
+    const float2 cs2 = make_float2(cs, cs);
     bool ok = true;
-    uint32_t it = 0, v_uses = 0;
-    uint32_t c = 0, cp = 0;                  // S tiles, P passes so far
-    for (int round = 0; unit_at<kCausal>(a, round, n_units, &u); ++round) {
+    uint32_t it = 0, joins = 0;
+    Turn h;
+    // O holds every half handed over so far (there is one)
+    auto o_ready = [&]() {
+      const int b = h.b == 0 ? kBuf - 1 : h.b - 1;
+      if (!wait_warp(&sm.o_done[t][b], h.b == 0 ? h.parity ^ 1 : h.parity))
+        return false;
+      tc_fence_after();
+      return true;
+    };
+    for (int round = 0;; ++round) {
       const int ub = round & 1;
-      const bool real = t * per + qi < u.b.tb;
-      const int limit =
-          kCausal ? u.b.first_limit + (real ? t * per + qi : u.b.tb - 1)
-                  : u.b.key_end - 1;
-      const int tile_limit = kCausal ? u.b.first_limit + t * per
-                                     : u.b.key_end - 1;
-      const bool exact = u.b.first_limit + 1 < kExactKeys;
+      if (!wait_warp(&sm.unit_full[ub], (round >> 1) & 1)) {
+        ok = false;
+        break;
+      }
+      const Unit& u = sm.unit[ub];
+      if (!u.live) break;
+      const int n_tiles = u.n_tiles, n = u.n[t], tile0 = u.e.tile0;
+      const int tb = u.b.tb, first_limit = u.b.first_limit;
+      const bool real = t * per + qi < tb;
+      const int limit = kCausal
+                            ? first_limit + (real ? t * per + qi : tb - 1)
+                            : u.b.key_end - 1;
+      const int tile_limit = kCausal ? first_limit + t * per : limit;
+      const bool exact = first_limit + 1 < kExactKeys;
       float m_run = -INFINITY, l_run = 0.f;
-      for (int j = 0; j < u.n_tiles; ++j, ++it) {
-        const int st = it % kST;
-        const uint32_t v_use = (v_uses >> st) & 1;
-        const bool edge = u.e.tile0 + j >= u.edge0;
-        if (edge) v_uses ^= 1u << st;
-        if (j >= u.n[t] || !ok) continue;
-        if (edge && !wait_warp(&sm.v_ready[st], v_use)) {
-          ok = false;   // (orders the notes in `poison` before the result)
-          continue;
-        }
-        const int key0 = (u.e.tile0 + j) * kBN;
-        if (!wait_warp(&sm.s_full[t], c & 1)) {
-          ok = false;
-          continue;
-        }
-        tc_fence_after();
-        float s[kBN];
-        tmem_ld128(s_addr, s);
-        const uint32_t bad = sm.bad_pages[st];
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(smem_u32(&sm.s_free[t]));
-        ++c;
-        if (bad != 0 || key0 + kBN - 1 > tile_limit) {
-#pragma unroll
-          for (int x = 0; x < kBN; ++x)
-            if (key0 + x > limit || ((bad >> (x / kPS)) & 1u))
-              s[x] = -INFINITY;
-        }
-        // ---- the tile's maximum; the offset moves when it grew by 2^8 -----------
-        float mx0 = -INFINITY, mx1 = -INFINITY;
-#pragma unroll
-        for (int x = 0; x < kBN; x += 4) {
-          mx0 = fmax3(mx0, s[x], s[x + 1]);
-          mx1 = fmax3(mx1, s[x + 2], s[x + 3]);
-        }
-        const float m_tile = fmaxf(mx0, mx1) * cs;   // scale > 0
-        const bool grow = m_tile > m_run + kLazy;
-        if (__any_sync(0xffffffffu, grow)) {
-          const float m_new = grow ? m_tile : m_run;
-          const float alpha = grow ? fast_exp2(m_run - m_new) : 1.f;
-          l_run *= alpha;
-          m_run = m_new;
-          if (j > 0) {
-            if (!wait_warp(&sm.o_done[t], (cp - 1) & 1)) {
-              ok = false;
-              continue;
-            }
-            tc_fence_after();
-            float o[64];
-            tmem_ld64(o_addr, o);
-#pragma unroll
-            for (int d = 0; d < 64; ++d) o[d] *= alpha;
-            tmem_st64(o_addr, o);
-          }
-        }
-        const float m_use = m_run == -INFINITY ? 0.f : m_run;
-        // ---- exponentials, their sum, P in bf16 ----------------------------------
-        const float2 cs2 = make_float2(cs, cs);
-        const float2 nm2 = make_float2(-m_use, -m_use);
-        float2 sum0 = make_float2(0.f, 0.f), sum1 = sum0;
-        float hi[64];
-#pragma unroll
-        for (int e = 0; e < 64; ++e) {
-          const float2 x =
-              __ffma2_rn(make_float2(s[2 * e], s[2 * e + 1]), cs2, nm2);
-          const float2 p = make_float2(fast_exp2(x.x), fast_exp2(x.y));
-          if (e & 1) sum1 = __fadd2_rn(sum1, p);
-          else sum0 = __fadd2_rn(sum0, p);
-          const uint32_t h = pack_bf16x2(p.x, p.y);
-          hi[e] = __uint_as_float(h);
-          if (exact) {
-            s[2 * e] = p.x - bf16_lo(h);
-            s[2 * e + 1] = p.y - bf16_hi(h);
-          }
-        }
-        l_run += (sum0.x + sum0.y) + (sum1.x + sum1.y);
-        // P's columns are free once the last pass has read them
-        if (cp > 0 && !wait_warp(&sm.o_done[t], (cp - 1) & 1)) {
-          ok = false;
-          continue;
-        }
-        tc_fence_after();
-        tmem_st64(p_addr, hi);
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(smem_u32(&sm.p_full[t]));
-        ++cp;
-        if (exact) {
-#pragma unroll
-          for (int e = 0; e < 64; ++e)
-            hi[e] = __uint_as_float(pack_bf16x2(s[2 * e], s[2 * e + 1]));
-          if (!wait_warp(&sm.o_done[t], (cp - 1) & 1)) {
+      // ---- the halves: two loads of 32 columns, the second in flight while the
+      //      first is exponentiated against the offset m_run as it stands, the
+      //      maximum beside it.  Halves with hidden keys, the first of a unit
+      //      and those where a row's maximum grew by 2^8 take the maximum
+      //      first, move the offset (rescaling O and the sum) and
+      //      exponentiate from the registers (again).  The loop's scalar code
+      //      is kept short: it costs as much time as the exponentials ------------
+      const int halves = ok ? 2 * n : 0;
+      const int plain = exact ? 0 : (tile_limit + 1 - tile0 * kBN) / kHalf;
+      volatile const int32_t* bad_unit = &sm.bad_unit[ub];
+#pragma unroll 1
+      for (int i = 0; i < halves; ++i) {
+          if (!wait_warp(&sm.s_full[t][h.b], h.parity)) {
             ok = false;
-            continue;
+            break;
           }
           tc_fence_after();
-          tmem_st64(p_addr, hi);
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(smem_u32(&sm.p_full[t]));
-          ++cp;
-        }
-      }
-
-      // ---- the unit's result ------------------------------------------------------
-      float o[64];
-      if (u.n[t] > 0 && ok) ok = wait_warp(&sm.o_done[t], (cp - 1) & 1);
-      if (u.n[t] > 0 && ok) {
-        tc_fence_after();
-        tmem_ld64(o_addr, o);
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(smem_u32(&sm.o_free[t]));
-      } else {
+          const uint32_t buf = s_addr + h.b * kHalf;
+          uint32_t x[32], y[32], hi[32];
+          tmem_ld32(buf, x);
+          tmem_wait32(x);
+          tmem_ld32(buf + 32, y);
+          bool again = i == 0 || i >= plain || *bad_unit;
+          float2 sum = make_float2(0.f, 0.f);
+          float mx[2] = {-INFINITY, -INFINITY};
+          float m_use = m_run;
+          auto scaled = [&](const uint32_t (&z)[32], int e) {
+            return __ffma2_rn(make_float2(__uint_as_float(z[2 * e]),
+                                          __uint_as_float(z[2 * e + 1])),
+                              cs2, make_float2(-m_use, -m_use));
+          };
+          auto maximum = [&](const uint32_t (&z)[32], int e) {
+            mx[e & 1] = fmax3(mx[e & 1], __uint_as_float(z[2 * e]),
+                              __uint_as_float(z[2 * e + 1]));
+          };
+          if (__builtin_expect(!again, 1)) {
+            auto quick = [&](const uint32_t (&z)[32], int base) {
 #pragma unroll
-        for (int d = 0; d < 64; ++d) o[d] = 0.f;
-        l_run = 0.f;
-        m_run = -INFINITY;
-      }
-      if (u.e.tile1 > u.edge0) {     // the unit had edge tiles
+              for (int e = 0; e < 16; ++e) {
+                const float2 v = scaled(z, e);
+                // the special function unit is the floor of this loop: every
+                // fourth pair goes through the FMA units
+                const float2 w = (e & 3) == 3
+                                     ? exp2_cubic(v)
+                                     : make_float2(fast_exp2(v.x),
+                                                   fast_exp2(v.y));
+                maximum(z, e);
+                sum = __fadd2_rn(sum, w);
+                hi[base + e] = pack_bf16x2(w.x, w.y);
+              }
+            };
+            quick(x, 0);
+            tmem_wait32(y);
+            quick(y, 16);
+          } else {
+            tmem_wait32(y);
+            const uint32_t bad =
+                (sm.bad_pages[(it + (i >> 1)) % kST] >> (4 * (i & 1))) & 15u;
+            const int key0 = tile0 * kBN + i * kHalf;
+            if (bad != 0 || key0 + kHalf - 1 > tile_limit) {
 #pragma unroll
-        for (int d = 0; d < 64; ++d)
-          if (sm.poison[ub][d] <= limit) o[d] = NAN;
-      }
-      bool write = real;
-      if (u.e.parts > 1) {
-        // leave (m, l, O); [dim / 4][row] float4, so that a warp's stores are
-        // contiguous
-        const size_t slot0 = (size_t)u.e.part_base * a.num_kv_heads + u.kvh;
-        auto part = [&](int k) {
-          return a.tile_parts +
-                 (slot0 + (size_t)k * a.num_kv_heads) * kTilePartFloats +
-                 t * (kTilePartFloats / 2);
-        };
-        float* mine = part(u.e.part);
-        __stcg(mine + r, m_run);
-        __stcg(mine + kBM + r, l_run);
-        float4* dst = reinterpret_cast<float4*>(mine + 2 * kBM) + r;
+              for (int k = 0; k < 32; ++k) {
+                if (key0 + k > limit || ((bad >> (k / kPS)) & 1u))
+                  x[k] = 0xff800000u;   // -inf
+                if (key0 + 32 + k > limit || ((bad >> (2 + k / kPS)) & 1u))
+                  y[k] = 0xff800000u;
+              }
+            }
 #pragma unroll
-        for (int d = 0; d < 16; ++d)
-          __stcg(dst + d * kBM, make_float4(o[4 * d], o[4 * d + 1],
-                                            o[4 * d + 2], o[4 * d + 3]));
-        asm volatile("bar.sync %0, 128;" ::"r"(1 + t) : "memory");
-        if ((threadIdx.x & 127) == 0) {
-          int32_t* counter = a.tile_counters + 2 * slot0 + t;
-          __threadfence();
-          sm.last[t] = atomicAdd(counter, 1) == u.e.parts - 1;
-          if (sm.last[t]) *counter = 0;
-          __threadfence();
-        }
-        asm volatile("bar.sync %0, 128;" ::"r"(1 + t) : "memory");
-        write = real && sm.last[t];
-        if (sm.last[t]) {
-          m_run = -INFINITY;
-          for (int k = 0; k < u.e.parts; ++k)
-            m_run = fmaxf(m_run, __ldcg(part(k) + r));
-          l_run = 0.f;
-#pragma unroll
-          for (int d = 0; d < 64; ++d) o[d] = 0.f;
-          for (int k = 0; k < u.e.parts; ++k) {
-            const float* p = part(k);
-            const float mk = __ldcg(p + r);
-            const float f = mk == m_run ? 1.f : fast_exp2(mk - m_run);
-            l_run = fmaf(__ldcg(p + kBM + r), f, l_run);
-            const float4* src =
-                reinterpret_cast<const float4*>(p + 2 * kBM) + r;
-#pragma unroll
-            for (int d = 0; d < 16; ++d) {
-              const float4 x = __ldcg(src + d * kBM);
-              o[4 * d] = fmaf(x.x, f, o[4 * d]);
-              o[4 * d + 1] = fmaf(x.y, f, o[4 * d + 1]);
-              o[4 * d + 2] = fmaf(x.z, f, o[4 * d + 2]);
-              o[4 * d + 3] = fmaf(x.w, f, o[4 * d + 3]);
+            for (int e = 0; e < 16; ++e) {
+              maximum(x, e);
+              maximum(y, e);
             }
           }
-        }
-      }
-      if (write) {
-        const float inv = l_run == 0.f ? 0.f : 1.f / l_run;   // NaN stays
-        uint4* dst = reinterpret_cast<uint4*>(
-            a.out + ((size_t)(u.b.q_row + t * per + qi) * a.num_q_heads +
-                     (u.kvh << a.group_shift) + hh) * kD);
+          const float m_half = fmaxf(mx[0], mx[1]) * cs;   // scale > 0
+          const bool grow = m_half > m_run + kLazy;
+          if (__builtin_expect(__any_sync(0xffffffffu, grow), 0)) {
+            again = true;
+            const float alpha = grow ? fast_exp2(m_run - m_half) : 1.f;
+            m_run = grow ? m_half : m_run;
+            l_run *= alpha;
+            if (i > 0) {
+              if (!o_ready()) {
+                ok = false;
+                break;
+              }
+#pragma unroll 1
+              for (int d0 = 0; d0 < kD; d0 += 16) {
+                uint32_t o[16];
+                tmem_ld16(o_addr + d0, o);
 #pragma unroll
-        for (int k = 0; k < kD / 8; ++k)
-          dst[k] = make_uint4(
+                for (int d = 0; d < 16; ++d)
+                  o[d] = __float_as_uint(__uint_as_float(o[d]) * alpha);
+                tmem_st16(o_addr + d0, o);
+              }
+            }
+          }
+          if (__builtin_expect(again, 0)) {
+            m_use = m_run == -INFINITY ? 0.f : m_run;
+            sum = make_float2(0.f, 0.f);
+#pragma unroll
+            for (int e = 0; e < 32; ++e) {
+              const float2 v = e < 16 ? scaled(x, e) : scaled(y, e - 16);
+              const float2 w = make_float2(fast_exp2(v.x), fast_exp2(v.y));
+              sum = __fadd2_rn(sum, w);
+              hi[e] = pack_bf16x2(w.x, w.y);
+              if (exact) {   // P's remainder, in the place of the scores
+                const uint32_t lo = pack_bf16x2(w.x - bf16_lo(hi[e]),
+                                                w.y - bf16_hi(hi[e]));
+                if (e < 16) x[e] = lo;
+                else y[e - 16] = lo;
+              }
+            }
+          }
+          l_run += sum.x + sum.y;
+          // P takes the place of S (the remainder behind it)
+          tmem_st32(buf, hi);
+          if (__builtin_expect(exact, 0)) {
+#pragma unroll
+            for (int e = 0; e < 32; ++e) hi[e] = e < 16 ? x[e] : y[e - 16];
+            tmem_st32(buf + 32, hi);
+          }
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(smem_u32(&sm.p_full[t][h.b]));
+          h.next();
+      }
+      it += n_tiles;
+
+      // ---- the unit's result, 32 dims at a time ------------------------------------
+      if (n > 0 && ok) ok = o_ready();
+      const bool any = n > 0 && ok;
+      if (!any) {
+        m_run = -INFINITY;
+        l_run = 0.f;
+      }
+      if (!wait_warp(&sm.clean[ub], (round >> 1) & 1)) ok = false;
+      const bool poisoned = sm.poisoned[ub] != 0;
+      const int parts = u.e.parts;
+      const size_t slot0 = (size_t)u.e.part_base * a.num_kv_heads + u.kvh;
+      // a part: m, l, then O as [dim / 4][row] float4, so that a warp's
+      // accesses are contiguous
+      auto part = [&](int k) {
+        return a.tile_parts +
+               (slot0 + (size_t)k * a.num_kv_heads) * kTilePartFloats +
+               t * (kTilePartFloats / 2);
+      };
+      uint4* dst = reinterpret_cast<uint4*>(
+          a.out + ((size_t)(u.b.q_row + t * per + qi) * a.num_q_heads +
+                   (u.kvh << a.group_shift) + hh) * kD);
+      auto write32 = [&](const float (&o)[32], int d0, float inv) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          dst[d0 / 8 + k] = make_uint4(
               pack_bf16x2(o[8 * k] * inv, o[8 * k + 1] * inv),
               pack_bf16x2(o[8 * k + 2] * inv, o[8 * k + 3] * inv),
               pack_bf16x2(o[8 * k + 4] * inv, o[8 * k + 5] * inv),
               pack_bf16x2(o[8 * k + 6] * inv, o[8 * k + 7] * inv));
+      };
+#pragma unroll 1
+      for (int d0 = 0; d0 < kD; d0 += 32) {
+        float o[32];
+        if (any) {
+          uint32_t x[32];
+          tmem_ld32(o_addr + d0, x);
+          tmem_wait32(x);
+#pragma unroll
+          for (int d = 0; d < 32; ++d) o[d] = __uint_as_float(x[d]);
+        } else {
+#pragma unroll
+          for (int d = 0; d < 32; ++d) o[d] = 0.f;
+        }
+        if (poisoned) {
+#pragma unroll
+          for (int d = 0; d < 32; ++d)
+            if (sm.poison[ub][d0 + d] <= limit) o[d] = NAN;
+        }
+        if (parts > 1) {
+          float4* to = reinterpret_cast<float4*>(part(u.e.part) + 2 * kBM) +
+                       d0 / 4 * kBM + r;
+#pragma unroll
+          for (int d = 0; d < 8; ++d)
+            __stcg(to + d * kBM, make_float4(o[4 * d], o[4 * d + 1],
+                                             o[4 * d + 2], o[4 * d + 3]));
+        } else if (real) {
+          write32(o, d0, l_run == 0.f ? 0.f : 1.f / l_run);   // NaN stays
+        }
+      }
+      if (any) {
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&sm.o_free[t]));
+      }
+      if (parts > 1) {
+        __stcg(part(u.e.part) + r, m_run);
+        __stcg(part(u.e.part) + kBM + r, l_run);
+        // the four warps' stores, then one count for the part
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&sm.part_in[t]));
+        if (quarter == 0 && lane == 0) {
+          bool last = false;
+          if (mbar_wait(smem_u32(&sm.part_in[t]), joins & 1)) {
+            int32_t* counter = a.tile_counters + 2 * slot0 + t;
+            __threadfence();
+            last = atomicAdd(counter, 1) == parts - 1;
+            if (last) *counter = 0;
+            __threadfence();
+          }
+          sm.last[t] = last;
+          mbar_arrive(smem_u32(&sm.part_out[t]));
+        }
+        if (!wait_warp(&sm.part_out[t], joins & 1)) ok = false;
+        ++joins;
+        if (ok && sm.last[t]) {
+          float M = -INFINITY, L = 0.f;
+          for (int k = 0; k < parts; ++k) M = fmaxf(M, __ldcg(part(k) + r));
+          // equal offsets first: -inf must not become NaN
+          auto factor = [&](int k) {
+            const float m = __ldcg(part(k) + r);
+            return m == M ? 1.f : fast_exp2(m - M);
+          };
+          for (int k = 0; k < parts; ++k)
+            L = fmaf(__ldcg(part(k) + kBM + r), factor(k), L);
+#pragma unroll 1
+          for (int d0 = 0; d0 < kD; d0 += 32) {
+            float o[32];
+#pragma unroll
+            for (int d = 0; d < 32; ++d) o[d] = 0.f;
+            for (int k = 0; k < parts; ++k) {
+              const float f = factor(k);
+              const float4* from =
+                  reinterpret_cast<const float4*>(part(k) + 2 * kBM) +
+                  d0 / 4 * kBM + r;
+#pragma unroll
+              for (int d = 0; d < 8; ++d) {
+                const float4 x = __ldcg(from + d * kBM);
+                o[4 * d] = fmaf(x.x, f, o[4 * d]);
+                o[4 * d + 1] = fmaf(x.y, f, o[4 * d + 1]);
+                o[4 * d + 2] = fmaf(x.z, f, o[4 * d + 2]);
+                o[4 * d + 3] = fmaf(x.w, f, o[4 * d + 3]);
+              }
+            }
+            if (real) write32(o, d0, L == 0.f ? 0.f : 1.f / L);
+          }
+        }
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(smem_u32(&sm.q_empty[ub]));

@@ -194,6 +194,7 @@ struct ChunkEntry {              // work of the tile kernel, for every KV head
 };
 struct ChunkPlan {
   int32_t entries;
+  int32_t next;                  // unit (entry x KV head) to be taken next
 };
 struct ChunkArgs {
   __nv_bfloat16* out;            // [rows][Hq][D]
