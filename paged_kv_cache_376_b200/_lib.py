@@ -148,19 +148,48 @@ def _stream(stream):
     return ctypes.c_void_p(stream.cuda_stream)
 
 
-def _launch(stream, *tensors):
-    """The device guard and stream pointer of a call on ``tensors`` (None
-    entries skipped): all of them on one device, the stream on it too."""
-    tensors = [t for t in tensors if t is not None]
-    dev = tensors[0].device
+# The calls below check about ten tensors each; at a few microseconds of GPU
+# time that is what a small call costs, so the checks are one pass over cheap
+# attributes, and the device and stream come from torch's plain accessors.
+def _one_device(tensors, stream):
+    """Device index and stream pointer of a call on ``tensors`` (None entries
+    skipped): all of them on one device, the stream on it too."""
+    dev = -1
     for t in tensors:
-        if t.device != dev:
-            raise ValueError(f"tensors on {dev} and {t.device} in one call")
+        if t is not None:
+            d = t.get_device()
+            if d != dev:
+                if dev >= 0:
+                    raise ValueError(f"tensors on cuda:{dev} and cuda:{d} in "
+                                     "one call")
+                dev = d
     if stream is None:
-        stream = torch.cuda.current_stream(dev)
-    elif stream.device != dev:
-        raise ValueError(f"stream on {stream.device}, tensors on {dev}")
-    return torch.cuda.device(dev), ctypes.c_void_p(stream.cuda_stream)
+        return dev, torch._C._cuda_getCurrentRawStream(dev)
+    if stream.device.index != dev:
+        raise ValueError(f"stream on {stream.device}, tensors on cuda:{dev}")
+    return dev, stream.cuda_stream
+
+
+def _all_cuda(dtype, **tensors):
+    for name, t in tensors.items():
+        if t is not None and not (isinstance(t, torch.Tensor) and t.is_cuda
+                                  and t.dtype is dtype and t.is_contiguous()):
+            _cuda(t, dtype, name)
+
+
+def _addr(t):
+    return None if t is None else t.data_ptr()
+
+
+def _call(what, dev, *args):
+    fn = getattr(load(), what)
+    if torch._C._cuda_getDevice() == dev:
+        status = fn(*args)
+    else:
+        with torch.cuda.device(dev):
+            status = fn(*args)
+    if status != TV_OK:
+        _check(status, what)
 
 
 def tv_kv_append(k_new, v_new, slot_mapping, k_pool, v_pool, err=None,
@@ -226,14 +255,14 @@ def _token_rows(t, name):
         raise TypeError(f"{name} must be a torch.Tensor")
     if not t.is_cuda:
         raise ValueError(f"{name} must be on a CUDA device")
-    if t.dtype != torch.bfloat16:
+    if t.dtype is not torch.bfloat16:
         raise TypeError(f"{name} must be {torch.bfloat16}, got {t.dtype}")
-    if t.dim() != 3 or (t.numel() and (
-            t.stride(2) != 1 or (t.shape[1] > 1
-                                 and t.stride(1) != t.shape[2]))):
-        raise ValueError(f"{name} must be [T][H][D] with contiguous heads")
-    row = t.shape[1] * t.shape[2]
-    return t.stride(0) if t.shape[0] > 1 else row
+    if t.dim() == 3:
+        n, h, d = t.shape
+        s0, s1, s2 = t.stride()
+        if n * h * d == 0 or (s2 == 1 and (h == 1 or s1 == d)):
+            return s0 if n > 1 else h * d
+    raise ValueError(f"{name} must be [T][H][D] with contiguous heads")
 
 
 def tv_kv_append_mrope(q_out, q, k_new, v_new, slot_mapping, positions,
@@ -244,22 +273,17 @@ def tv_kv_append_mrope(q_out, q, k_new, v_new, slot_mapping, positions,
     table as tv_kv_append_rope), q into q_out [T][Hq][D], K and V into their
     slots.  q, k_new, v_new [T][H][D] may have strided token rows; positions
     is [axes][T], pair_axis [D/2] int32.  q and q_out None: K and V only."""
-    lib = load()
     if (q is None) != (q_out is None):
         raise ValueError("q and q_out go together")
     ks, vs = _token_rows(k_new, "k_new"), _token_rows(v_new, "v_new")
-    bf, i32 = torch.bfloat16, torch.int32
-    _cuda(k_pool, bf, "k_pool"), _cuda(v_pool, bf, "v_pool")
-    _cuda(slot_mapping, i32, "slot_mapping"), _cuda(positions, i32,
-                                                    "positions")
-    _cuda(pair_axis, i32, "pair_axis")
-    if err is not None:
-        _cuda(err, i32, "err")
+    _all_cuda(torch.bfloat16, k_pool=k_pool, v_pool=v_pool, q_out=q_out)
+    _all_cuda(torch.int32, slot_mapping=slot_mapping, positions=positions,
+              pair_axis=pair_axis, err=err)
     num_pages, page_size, hkv, d = k_pool.shape
     t = k_new.shape[0]
     if v_pool.shape != k_pool.shape or k_new.shape != v_new.shape:
         raise ValueError("K/V shape mismatch")
-    if k_new.shape[1:] != (hkv, d) or slot_mapping.shape != (t,) or \
+    if k_new.shape != (t, hkv, d) or slot_mapping.shape != (t,) or \
             positions.dim() != 2 or positions.shape[1] != t or \
             pair_axis.shape != (d // 2,):
         raise ValueError("k_new must be [T][Hkv][D] with slot_mapping [T], "
@@ -267,20 +291,18 @@ def tv_kv_append_mrope(q_out, q, k_new, v_new, slot_mapping, positions,
     qs, hq = 0, 0
     if q is not None:
         qs = _token_rows(q, "q")
-        _cuda(q_out, bf, "q_out")
         hq = q.shape[1]
         if q.shape != (t, hq, d) or q_out.shape != q.shape:
             raise ValueError("q and q_out must be [T][Hq][D]")
     max_pos = _rope_table(cos_sin, d)
-    guard, st = _launch(stream, k_pool, v_pool, k_new, v_new, q, q_out,
-                        slot_mapping, positions, pair_axis, cos_sin, err)
-    with guard:
-        _check(lib.tv_kv_append_mrope(
-            _ptr(q_out), _ptr(q), qs, _ptr(k_new), ks, _ptr(v_new), vs,
-            _ptr(slot_mapping), _ptr(positions), positions.shape[0],
-            _ptr(pair_axis), t, _ptr(k_pool), _ptr(v_pool), num_pages, hq,
-            hkv, d, page_size, _ptr(cos_sin), max_pos, _ptr(err), st),
-            "tv_kv_append_mrope")
+    dev, st = _one_device((k_pool, v_pool, k_new, v_new, q, q_out,
+                           slot_mapping, positions, pair_axis, cos_sin, err),
+                          stream)
+    _call("tv_kv_append_mrope", dev, _addr(q_out), _addr(q), qs,
+          k_new.data_ptr(), ks, v_new.data_ptr(), vs, slot_mapping.data_ptr(),
+          positions.data_ptr(), positions.shape[0], pair_axis.data_ptr(), t,
+          k_pool.data_ptr(), v_pool.data_ptr(), num_pages, hq, hkv, d,
+          page_size, cos_sin.data_ptr(), max_pos, _addr(err), st)
 
 
 def tv_paged_decode_append_rope(out, q, k_new, v_new, k_pool, v_pool,
@@ -482,18 +504,13 @@ def chunk_workspace(num_seqs, max_query_len, num_q_heads, num_kv_heads,
 
 def _chunk(name, out, q, query_start_loc, k_pool, v_pool, block_tables, lens,
            lens_name, scale, max_query_len, workspace, err, stream):
-    lib = load()
-    bf = torch.bfloat16
-    for n, t in (("out", out), ("q", q), ("k_pool", k_pool),
-                 ("v_pool", v_pool)):
-        _cuda(t, bf, n)
-    for n, t in (("query_start_loc", query_start_loc),
-                 ("block_tables", block_tables), (lens_name, lens)):
-        _cuda(t, torch.int32, n)
-    if err is not None:
-        _cuda(err, torch.int32, "err")
+    _all_cuda(torch.bfloat16, out=out, q=q, k_pool=k_pool, v_pool=v_pool)
+    _all_cuda(torch.int32, query_start_loc=query_start_loc,
+              block_tables=block_tables, err=err, **{lens_name: lens})
+    size = 0
     if workspace is not None:
-        _cuda(workspace, torch.uint8, "workspace")
+        _all_cuda(torch.uint8, workspace=workspace)
+        size = workspace.numel()
     num_pages, page_size, hkv, d = k_pool.shape
     rows, hq, qd = q.shape
     b = lens.shape[0]
@@ -501,16 +518,13 @@ def _chunk(name, out, q, query_start_loc, k_pool, v_pool, block_tables, lens,
             lens.dim() != 1 or query_start_loc.shape != (b + 1,) or \
             block_tables.dim() != 2 or block_tables.shape[0] != b:
         raise ValueError("shape mismatch")
-    guard, st = _launch(stream, q, out, query_start_loc, k_pool, v_pool,
-                        block_tables, lens, workspace, err)
-    with guard:
-        _check(getattr(lib, name)(
-            _ptr(out), _ptr(q), rows, _ptr(query_start_loc), _ptr(k_pool),
-            _ptr(v_pool), _ptr(block_tables), block_tables.shape[1],
-            _ptr(lens), b, int(max_query_len), hq, hkv, d, page_size,
-            num_pages, float(scale), _ptr(workspace),
-            workspace.numel() if workspace is not None else 0, _ptr(err), st),
-            name)
+    dev, st = _one_device((q, out, query_start_loc, k_pool, v_pool,
+                           block_tables, lens, workspace, err), stream)
+    _call(name, dev, out.data_ptr(), q.data_ptr(), rows,
+          query_start_loc.data_ptr(), k_pool.data_ptr(), v_pool.data_ptr(),
+          block_tables.data_ptr(), block_tables.shape[1], lens.data_ptr(), b,
+          int(max_query_len), hq, hkv, d, page_size, num_pages, float(scale),
+          _addr(workspace), size, _addr(err), st)
 
 
 def tv_paged_chunk(out, q, query_start_loc, k_pool, v_pool, block_tables,
@@ -719,21 +733,16 @@ def tv_pool_truncate(state, block_tables, context_lens, new_lens, err=None,
                      stream=None):
     """Every sequence keeps its first new_lens[s] tokens; pages behind them
     that nobody else holds go back to the pool."""
-    lib = load()
     num_pages = _pool_pages(state)
     mb, b = _pool_tables(block_tables, context_lens)
-    _cuda(new_lens, torch.int32, "new_lens")
+    _all_cuda(torch.int32, new_lens=new_lens, err=err)
     if new_lens.shape != context_lens.shape:
         raise ValueError("new_lens and context_lens differ in length")
-    if err is not None:
-        _cuda(err, torch.int32, "err")
-    guard, st = _launch(stream, state, block_tables, context_lens, new_lens,
-                        err)
-    with guard:
-        _check(lib.tv_pool_truncate(
-            _ptr(state), num_pages, _ptr(block_tables), mb,
-            _ptr(context_lens), _ptr(new_lens), b, _ptr(err), st),
-            "tv_pool_truncate")
+    dev, st = _one_device((state, block_tables, context_lens, new_lens, err),
+                          stream)
+    _call("tv_pool_truncate", dev, state.data_ptr(), num_pages,
+          block_tables.data_ptr(), mb, context_lens.data_ptr(),
+          new_lens.data_ptr(), b, _addr(err), st)
 
 
 def pool_moves(num_pages, device=None):
@@ -750,59 +759,47 @@ def tv_pool_compact(state, block_tables, context_lens, moves, num_moves,
     """Pages in use move to the front of the pool; moves[0][:n] -> moves[1][:n]
     with n = num_moves (see pool_moves) lists them for tv_page_copy on further
     layers' pools.  page_size is the pools' when they are given."""
-    lib = load()
     num_pages = _pool_pages(state)
     mb, b = _pool_tables(block_tables, context_lens)
-    _cuda(moves, torch.int32, "moves"), _cuda(num_moves, torch.int32,
-                                              "num_moves")
+    _all_cuda(torch.int32, moves=moves, num_moves=num_moves, err=err)
     if moves.dim() != 2 or moves.shape[0] != 2 or num_moves.numel() < 1:
         raise ValueError("moves must be [2][max_moves], num_moves [1]")
     if (k_pool is None) != (v_pool is None):
         raise ValueError("k_pool and v_pool go together")
     ps, hkv, d = page_size or 16, 1, 64
     if k_pool is not None:
-        _cuda(k_pool, torch.bfloat16, "k_pool")
-        _cuda(v_pool, torch.bfloat16, "v_pool")
+        _all_cuda(torch.bfloat16, k_pool=k_pool, v_pool=v_pool)
         if k_pool.shape[0] != num_pages or v_pool.shape != k_pool.shape:
             raise ValueError("pool_state and the pools disagree on num_pages")
         if page_size not in (None, k_pool.shape[1]):
             raise ValueError("page_size is not the pools'")
         _, ps, hkv, d = k_pool.shape
-    if err is not None:
-        _cuda(err, torch.int32, "err")
-    guard, st = _launch(stream, state, block_tables, context_lens, moves,
-                        num_moves, k_pool, v_pool, err)
-    with guard:
-        _check(lib.tv_pool_compact(
-            _ptr(state), num_pages, _ptr(block_tables), mb,
-            _ptr(context_lens), b, _ptr(moves[0]), _ptr(moves[1]),
-            moves.shape[1], _ptr(num_moves), _ptr(k_pool), _ptr(v_pool), hkv,
-            d, ps, _ptr(err), st), "tv_pool_compact")
+    dev, st = _one_device((state, block_tables, context_lens, moves,
+                           num_moves, k_pool, v_pool, err), stream)
+    cap = moves.shape[1]
+    _call("tv_pool_compact", dev, state.data_ptr(), num_pages,
+          block_tables.data_ptr(), mb, context_lens.data_ptr(), b,
+          moves.data_ptr(), moves.data_ptr() + 4 * cap, cap,
+          num_moves.data_ptr(), _addr(k_pool), _addr(v_pool), hkv, d, ps,
+          _addr(err), st)
 
 
 def tv_page_copy(k_pool, v_pool, src_pages, dst_pages, num_pairs=None,
                  err=None, stream=None):
     """Copy whole pages src_pages[i] -> dst_pages[i] of both pools, all of
     them or the first num_pairs (a device int32)."""
-    lib = load()
-    _cuda(k_pool, torch.bfloat16, "k_pool"), _cuda(v_pool, torch.bfloat16,
-                                                   "v_pool")
-    _cuda(src_pages, torch.int32, "src_pages")
-    _cuda(dst_pages, torch.int32, "dst_pages")
-    for n, t in (("num_pairs", num_pairs), ("err", err)):
-        if t is not None:
-            _cuda(t, torch.int32, n)
+    _all_cuda(torch.bfloat16, k_pool=k_pool, v_pool=v_pool)
+    _all_cuda(torch.int32, src_pages=src_pages, dst_pages=dst_pages,
+              num_pairs=num_pairs, err=err)
     if v_pool.shape != k_pool.shape or src_pages.dim() != 1 or \
             src_pages.shape != dst_pages.shape:
         raise ValueError("shape mismatch")
     num_pages, ps, hkv, d = k_pool.shape
-    guard, st = _launch(stream, k_pool, v_pool, src_pages, dst_pages,
-                        num_pairs, err)
-    with guard:
-        _check(lib.tv_page_copy(
-            _ptr(k_pool), _ptr(v_pool), num_pages, _ptr(src_pages),
-            _ptr(dst_pages), src_pages.numel(), _ptr(num_pairs), hkv, d, ps,
-            _ptr(err), st), "tv_page_copy")
+    dev, st = _one_device((k_pool, v_pool, src_pages, dst_pages, num_pairs,
+                           err), stream)
+    _call("tv_page_copy", dev, k_pool.data_ptr(), v_pool.data_ptr(),
+          num_pages, src_pages.data_ptr(), dst_pages.data_ptr(),
+          src_pages.numel(), _addr(num_pairs), hkv, d, ps, _addr(err), st)
 
 
 def tv_decode_step(state, out, q, k_new, v_new, k_pool, v_pool, block_tables,

@@ -103,9 +103,10 @@ __global__ void __launch_bounds__(256)
 // entries), the lanes exchange them by shuffles, and every lane turns the
 // vector pair u = lane & 3 (dimensions 8u .. 8u + 7 with + 32) of heads
 // lane >> 2, + 8, + 16, ... , so the angles are read once per token however
-// many heads it has.
+// many heads it has.  The first heads' vectors are loaded before the angles,
+// whose two lookups depend on one another.
 template <int kHeads>   // heads of a lane in flight at once
-__global__ void __launch_bounds__(256)
+__global__ void __launch_bounds__(128)
     kv_append_mrope_kernel(const MropeArgs a) {
   const int lane = threadIdx.x & 31;
   const int u = lane & 3;
@@ -113,10 +114,26 @@ __global__ void __launch_bounds__(256)
   const int axis = a.pair_axis[lane];
   const bool axis_ok = axis >= 0 && axis < a.num_axes;
   const int64_t stride = (int64_t)gridDim.x * (blockDim.x >> 5);
+  uint4 lo[kHeads], hi[kHeads];
+  auto load = [&](int64_t t, int h0) {
+#pragma unroll
+    for (int n = 0; n < kHeads; ++n) {
+      const int h = h0 + 8 * n;
+      if (h >= heads) continue;
+      const int hk = h - a.num_q_heads, hv = hk - a.num_kv_heads;
+      const __nv_bfloat16* src =
+          hk < 0   ? a.q + t * a.q_stride + h * 64
+          : hv < 0 ? a.k_new + t * a.k_stride + hk * 64
+                   : a.v_new + t * a.v_stride + hv * 64;
+      lo[n] = reinterpret_cast<const uint4*>(src)[u];
+      hi[n] = reinterpret_cast<const uint4*>(src)[u + 4];
+    }
+  };
   for (int64_t t = blockIdx.x * (int64_t)(blockDim.x >> 5) + (threadIdx.x >> 5);
        t < a.num_tokens; t += stride) {
     const int64_t slot = a.slot_mapping[t];
     const int pos = axis_ok ? a.positions[axis * a.num_tokens + t] : -1;
+    load(t, lane >> 2);
     if (slot < 0) continue;                  // padding
     const bool slot_ok = slot < a.num_slots;
     // a token turns as a whole or, with a bad position, not at all
@@ -137,19 +154,7 @@ __global__ void __launch_bounds__(256)
       s8[k] = __shfl_sync(0xffffffffu, sl, 8 * u + k);
     }
     for (int h0 = lane >> 2; h0 < heads; h0 += 8 * kHeads) {
-      uint4 lo[kHeads], hi[kHeads];
-#pragma unroll
-      for (int n = 0; n < kHeads; ++n) {
-        const int h = h0 + 8 * n;
-        if (h >= heads) continue;
-        const int hk = h - a.num_q_heads, hv = hk - a.num_kv_heads;
-        const __nv_bfloat16* src =
-            hk < 0   ? a.q + t * a.q_stride + h * 64
-            : hv < 0 ? a.k_new + t * a.k_stride + hk * 64
-                     : a.v_new + t * a.v_stride + hv * 64;
-        lo[n] = reinterpret_cast<const uint4*>(src)[u];
-        hi[n] = reinterpret_cast<const uint4*>(src)[u + 4];
-      }
+      if (h0 >= 8 * kHeads) load(t, h0);
 #pragma unroll
       for (int n = 0; n < kHeads; ++n) {
         const int h = h0 + 8 * n;
@@ -172,13 +177,10 @@ __global__ void __launch_bounds__(256)
 
 cudaError_t launch_kv_append_mrope(const MropeArgs& a, cudaStream_t stream) {
   if (a.num_tokens == 0) return cudaSuccess;
-  int dev = 0, sms = 148;
-  cudaGetDevice(&dev);
-  cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-  const int64_t want = (a.num_tokens + 7) / 8;
-  const int64_t cap = (int64_t)sms * 8;
+  const int64_t want = (a.num_tokens + 3) / 4;
+  const int64_t cap = (int64_t)device_sm_count() * 64;
   kv_append_mrope_kernel<3>
-      <<<(int)(want < cap ? want : cap), 256, 0, stream>>>(a);
+      <<<(int)(want < cap ? want : cap), 128, 0, stream>>>(a);
   return cudaGetLastError();
 }
 

@@ -397,39 +397,78 @@ __global__ void __launch_bounds__(kThreads, 1)
 // reference, and those that nobody holds any more go back on the stack in
 // ascending id order, as in a release.
 //
-// Bound: latency (a few integers per dropped page).  One warp per sequence, a
-// lane per dropped page; the freed pages are marked in a bitmap (one bit per
-// page, in the scratch words), whose order is the id order, so a scan over
-// num_pages / 32 words replaces a sort.
+// Bound: latency (a few integers per dropped page; chains of context -> entry
+// -> count -> mark).  16 lanes per sequence, four pages of each in flight, 64
+// sequences a CTA; the freed pages are marked in a bitmap (one bit per page, in
+// scratch words), whose order is the id order, so a scan over num_pages / 32
+// words by the CTA that ends last replaces a sort.  1024 sequences that drop
+// half of up to 256 pages: one CTA 68 us, this 13 us.
+constexpr int kSeqLanes = 16;
+constexpr int kSeqsPerCta = kThreads / kSeqLanes;
+
 __global__ void __launch_bounds__(kThreads, 1)
     pool_truncate_kernel(PoolView p, int32_t* bt, int mb, int32_t* ctx,
                          const int32_t* new_lens, int num_seqs,
                          uint32_t* err) {
   __shared__ int sh[33];
+  __shared__ bool last_cta;
   const int kPS = *p.page_size;
-  const int lane = threadIdx.x & 31;
+  const int top0 = *p.top;
+  const int lane = threadIdx.x % kSeqLanes;
+  const int s = blockIdx.x * kSeqsPerCta + threadIdx.x / kSeqLanes;
   uint32_t* marks = reinterpret_cast<uint32_t*>(p.cnt_app);
-  for (int s = threadIdx.x >> 5; s < num_seqs; s += kThreads / 32) {
-    const int c = ctx[s], n = new_lens[s];
+  int c = 0, n = 0;
+  if (s < num_seqs) {
+    c = ctx[s];
+    n = new_lens[s];
     if (c < 0 || c > mb * kPS || n < 0 || n > c) {
       if (lane == 0) flag_error(err, DEVERR_BAD_CONTEXT);
-      continue;
+      c = n = -1;
     }
-    const int last = pages_for(c, kPS);
-    for (int k = pages_for(n, kPS) + lane; k < last; k += 32) {
-      const int page = bt[(size_t)s * mb + k];
-      bt[(size_t)s * mb + k] = -1;
-      if (page < 0 || page >= p.num_pages)
-        flag_error(err, DEVERR_BAD_PAGE);
-      else if (atomicSub(p.ref + page, 1) == 1)
-        atomicOr(marks + (page >> 5), 1u << (page & 31));
+  }
+  __syncwarp();   // every lane has read the context
+  if (s < num_seqs && c >= 0) {
+    int32_t* row = bt + (size_t)s * mb;
+    const int end = pages_for(c, kPS);
+    constexpr int kU = 4;
+    for (int k0 = pages_for(n, kPS) + lane; k0 < end; k0 += kU * kSeqLanes) {
+      int page[kU], left[kU];
+#pragma unroll
+      for (int u = 0; u < kU; ++u) {
+        const int k = k0 + u * kSeqLanes;
+        page[u] = k < end ? row[k] : INT32_MAX;
+      }
+#pragma unroll
+      for (int u = 0; u < kU; ++u) {
+        const int k = k0 + u * kSeqLanes;
+        left[u] = 0;
+        if (k >= end) continue;
+        row[k] = -1;
+        if (page[u] < 0 || page[u] >= p.num_pages)
+          flag_error(err, DEVERR_BAD_PAGE);
+        else
+          left[u] = atomicSub(p.ref + page[u], 1);
+      }
+#pragma unroll
+      for (int u = 0; u < kU; ++u)
+        if (left[u] == 1) atomicOr(marks + (page[u] >> 5), 1u << (page[u] & 31));
     }
-    __syncwarp();
     if (lane == 0) ctx[s] = n;
   }
   __syncthreads();
+  if (gridDim.x > 1) {
+    // the CTA that ends last goes on (the count is a scratch word too)
+    if (threadIdx.x == 0) {
+      __threadfence();
+      last_cta = atomicAdd(p.last_app, 1) == (int)gridDim.x - 1;
+      if (last_cta) *p.last_app = 0;
+      __threadfence();
+    }
+    __syncthreads();
+    if (!last_cta) return;
+  }
   const int words = (p.num_pages + 31) / 32;
-  int top = *p.top;
+  int top = top0;
   for (int w0 = 0; w0 < words; w0 += kThreads) {
     const int w = w0 + threadIdx.x;
     uint32_t bits = w < words ? __ldcg(marks + w) : 0u;
@@ -445,7 +484,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     top += tot;
   }
-  __syncthreads();
   if (threadIdx.x == 0) *p.top = min(top, p.num_pages);
 }
 
@@ -453,13 +491,18 @@ __global__ void __launch_bounds__(kThreads, 1)
 // With U pages in use (count > 0), the i-th used page at or above U moves to
 // the i-th free page below U; both lists are ascending and equally long.  Then
 // the pages in use are exactly 0 .. U - 1 and the free stack is rebuilt as init
-// leaves it.  This kernel (one CTA) plans: counts as bit words, their scan, the
-// move lists, the counts and the stack.
+// leaves it.  This kernel (one CTA, latency-bound) plans: counts as bit words,
+// eight words a warp in flight, their scan, the move lists, the counts and the
+// stack.
+constexpr int kHeldWords = 4096;   // bit words kept in shared memory
+
 __global__ void __launch_bounds__(kThreads, 1)
     pool_compact_plan_kernel(PoolView p, int page_size, int32_t* move_src,
                              int32_t* move_dst, int32_t* num_moves,
                              uint32_t* err) {
   __shared__ int sh[33];
+  __shared__ uint32_t sh_held[kHeldWords];
+  let_next_kernel_start();
   const int n = p.num_pages;
   const int words = (n + 31) / 32;
   if (*p.page_size != page_size) {   // pools of another page size
@@ -469,14 +512,26 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     return;
   }
-  uint32_t* held = reinterpret_cast<uint32_t*>(p.cnt_app);
+  const bool on_chip = words <= kHeldWords;
+  uint32_t* held =
+      on_chip ? sh_held : reinterpret_cast<uint32_t*>(p.cnt_app);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   int mine = 0;
-  for (int i = threadIdx.x; i < 32 * words; i += kThreads) {
-    const uint32_t b =
-        __ballot_sync(0xffffffffu, i < n && p.ref[i] > 0);
-    if ((threadIdx.x & 31) == 0) {
-      held[i >> 5] = b;
-      mine += __popc(b);
+  constexpr int kU = 8;
+  for (int w0 = warp * kU; w0 < words; w0 += kU * (kThreads / 32)) {
+    int r[kU];
+#pragma unroll
+    for (int u = 0; u < kU; ++u) {
+      const int i = 32 * (w0 + u) + lane;
+      r[u] = i < n ? p.ref[i] : 0;
+    }
+#pragma unroll
+    for (int u = 0; u < kU; ++u) {
+      const uint32_t b = __ballot_sync(0xffffffffu, r[u] > 0);
+      if (lane == u && w0 + u < words) {
+        held[w0 + u] = b;
+        mine += __popc(b);
+      }
     }
   }
   int used;
@@ -487,7 +542,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint32_t src = 0, dst = 0;
     if (w < words) {
       const uint32_t b = held[w];
-      held[w] = 0;
+      if (!on_chip) held[w] = 0;
       // bits of this word whose page id is below `used`
       const int k = used - 32 * w;
       const uint32_t low = k >= 32 ? 0xffffffffu : k <= 0 ? 0u : (1u << k) - 1;
@@ -518,16 +573,16 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 // Block-table entries follow their pages: a binary search in the ascending
 // list of moved pages (entries below its first page did not move).
-__global__ void __launch_bounds__(256)
-    pool_compact_tables_kernel(int32_t* bt, int mb, const int32_t* ctx,
-                               int num_seqs, int kPS, const int32_t* move_src,
-                               const int32_t* move_dst,
-                               const int32_t* num_moves, uint32_t* err) {
-  const int n = *num_moves;
-  const int first = n > 0 ? move_src[0] : 0;
+__device__ __forceinline__ void move_entries(int32_t* bt, int mb,
+                                             const int32_t* ctx, int num_seqs,
+                                             int kPS, const int32_t* move_src,
+                                             const int32_t* move_dst, int n,
+                                             int cta, int ctas,
+                                             uint32_t* err) {
+  const int first = n > 0 ? __ldcg(move_src) : 0;
   const int64_t total = (int64_t)num_seqs * mb;
-  for (int64_t i = blockIdx.x * (int64_t)blockDim.x + threadIdx.x; i < total;
-       i += (int64_t)gridDim.x * blockDim.x) {
+  for (int64_t i = cta * (int64_t)blockDim.x + threadIdx.x; i < total;
+       i += (int64_t)ctas * blockDim.x) {
     const int s = (int)(i / mb), b = (int)(i % mb);
     int c = ctx[s];
     if (c < 0 || c > mb * kPS) {
@@ -540,51 +595,96 @@ __global__ void __launch_bounds__(256)
     int lo = 0, hi = n;             // first entry >= page
     while (lo < hi) {
       const int mid = (lo + hi) >> 1;
-      if (__ldg(move_src + mid) < page) lo = mid + 1;
+      if (__ldcg(move_src + mid) < page) lo = mid + 1;
       else hi = mid;
     }
-    if (lo < n && move_src[lo] == page) bt[i] = move_dst[lo];
+    if (lo < n && __ldcg(move_src + lo) == page) bt[i] = __ldcg(move_dst + lo);
   }
 }
 
 // Whole pages of K and V, src[i] to dst[i]: HBM-bound (2 x the bytes moved).
-// A unit is 16 KB of one tensor: 256 threads x four 16-byte vectors in flight.
+// A unit is 8 KB of one tensor: 256 threads x two 16-byte vectors, the next
+// unit's page ids in flight beside them.
+constexpr int kUnitVecs = 512;
+
+__device__ __forceinline__ void copy_pages(uint4* k_pool, uint4* v_pool,
+                                           int num_pages, int page_vecs,
+                                           const int32_t* src,
+                                           const int32_t* dst, int64_t n,
+                                           int64_t cta, int64_t ctas,
+                                           uint32_t* err) {
+  const int per = (page_vecs + kUnitVecs - 1) / kUnitVecs;   // units of a page
+  const int64_t units = n * 2 * per;
+  int a = 0, b = 0;
+  if (cta < units) {
+    a = __ldcg(src + cta / (2 * per));
+    b = __ldcg(dst + cta / (2 * per));
+  }
+  for (int64_t i = cta; i < units; i += ctas) {
+    const int r = (int)(i % (2 * per));
+    const int from_page = a, to_page = b;
+    if (i + ctas < units) {
+      a = __ldcg(src + (i + ctas) / (2 * per));
+      b = __ldcg(dst + (i + ctas) / (2 * per));
+    }
+    if (from_page < 0 || from_page >= num_pages || to_page < 0 ||
+        to_page >= num_pages) {
+      if (threadIdx.x == 0 && r == 0) flag_error(err, DEVERR_BAD_PAGE);
+      continue;
+    }
+    uint4* pool = r < per ? k_pool : v_pool;
+    const int v0 = (r < per ? r : r - per) * kUnitVecs + threadIdx.x;
+    const uint4* from = pool + (size_t)from_page * page_vecs;
+    uint4* to = pool + (size_t)to_page * page_vecs;
+    uint4 x[2];
+#pragma unroll
+    for (int k = 0; k < 2; ++k)
+      if (v0 + 256 * k < page_vecs) x[k] = __ldcs(from + v0 + 256 * k);
+#pragma unroll
+    for (int k = 0; k < 2; ++k)
+      if (v0 + 256 * k < page_vecs) __stcs(to + v0 + 256 * k, x[k]);
+  }
+}
+
 __global__ void __launch_bounds__(256)
     page_copy_kernel(uint4* k_pool, uint4* v_pool, int num_pages,
                      int page_vecs, const int32_t* src, const int32_t* dst,
                      int64_t max_pairs, const int32_t* num_pairs,
                      uint32_t* err) {
-  constexpr int kUnit = 1024;
   int64_t n = max_pairs;
   if (num_pairs) {
     n = *num_pairs;
     n = n < 0 ? 0 : (n > max_pairs ? max_pairs : n);
   }
-  const int per = (page_vecs + kUnit - 1) / kUnit;   // units of a page
-  for (int64_t i = blockIdx.x; i < n * 2 * per; i += gridDim.x) {
-    const int64_t pair = i / (2 * per);
-    const int r = (int)(i - pair * 2 * per);
-    const int a = src[pair], b = dst[pair];
-    if (a < 0 || a >= num_pages || b < 0 || b >= num_pages) {
-      if (threadIdx.x == 0 && r == 0) flag_error(err, DEVERR_BAD_PAGE);
-      continue;
-    }
-    uint4* pool = r < per ? k_pool : v_pool;
-    const int v0 = (r < per ? r : r - per) * kUnit;
-    const uint4* from = pool + (size_t)a * page_vecs + v0;
-    uint4* to = pool + (size_t)b * page_vecs + v0;
-    uint4 x[4];
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const int v = threadIdx.x + 256 * k;
-      if (v0 + v < page_vecs) x[k] = from[v];
-    }
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const int v = threadIdx.x + 256 * k;
-      if (v0 + v < page_vecs) to[v] = x[k];
-    }
-  }
+  copy_pages(k_pool, v_pool, num_pages, page_vecs, src, dst, n, blockIdx.x,
+             gridDim.x, err);
+}
+
+// What the plan leaves to do, in one launch that starts beside the plan: the
+// first table_ctas CTAs move the entries, the others copy pages.
+__global__ void __launch_bounds__(256)
+    pool_compact_move_kernel(int32_t* bt, int mb, const int32_t* ctx,
+                             int num_seqs, int kPS, int table_ctas,
+                             const int32_t* move_src, const int32_t* move_dst,
+                             const int32_t* num_moves, uint4* k_pool,
+                             uint4* v_pool, int num_pages, int page_vecs,
+                             uint32_t* err) {
+  wait_for_last_kernel();
+  const int n = __ldcg(num_moves);
+  if ((int)blockIdx.x < table_ctas)
+    move_entries(bt, mb, ctx, num_seqs, kPS, move_src, move_dst, n,
+                 blockIdx.x, table_ctas, err);
+  else
+    copy_pages(k_pool, v_pool, num_pages, page_vecs, move_src, move_dst, n,
+               blockIdx.x - table_ctas, gridDim.x - table_ctas, err);
+}
+
+// CTAs of a page copy: eight a SM are resident, more even the last wave out.
+int copy_ctas(int64_t max_pairs, int page_vecs) {
+  const int64_t want =
+      max_pairs * 2 * ((page_vecs + kUnitVecs - 1) / kUnitVecs);
+  const int64_t cap = (int64_t)device_sm_count() * 8;
+  return (int)(want < cap ? want : cap);
 }
 
 }  // namespace
@@ -593,8 +693,9 @@ cudaError_t launch_pool_truncate(int32_t* state, int num_pages, int32_t* bt,
                                  int mb, int32_t* ctx, const int32_t* new_lens,
                                  int num_seqs, uint32_t* err,
                                  cudaStream_t stream) {
-  pool_truncate_kernel<<<1, kThreads, 0, stream>>>(
-      view(state, num_pages), bt, mb, ctx, new_lens, num_seqs, err);
+  pool_truncate_kernel<<<(num_seqs + kSeqsPerCta - 1) / kSeqsPerCta, kThreads,
+                         0, stream>>>(view(state, num_pages), bt, mb, ctx,
+                                      new_lens, num_seqs, err);
   return cudaGetLastError();
 }
 
@@ -608,22 +709,18 @@ cudaError_t launch_pool_compact(int32_t* state, int num_pages, int page_size,
       view(state, num_pages), page_size, move_src, move_dst, num_moves, err);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
-  int dev = 0, sms = 148;
-  cudaGetDevice(&dev);
-  cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
   const int64_t want = ((int64_t)num_seqs * mb + 255) / 256;
-  const int64_t cap = (int64_t)sms * 8;
-  if (num_seqs > 0) {
-    pool_compact_tables_kernel<<<(int)(want < cap ? want : cap), 256, 0,
-                                 stream>>>(bt, mb, ctx, num_seqs, page_size,
-                                           move_src, move_dst, num_moves, err);
-    e = cudaGetLastError();
-    if (e != cudaSuccess) return e;
-  }
-  if (!k_pool) return cudaSuccess;
-  return launch_page_copy(k_pool, v_pool, num_pages, page_size * row_bytes,
-                          move_src, move_dst, num_pages / 2, num_moves, err,
-                          stream);
+  const int64_t cap = (int64_t)device_sm_count() * 2;
+  const int table_ctas = (int)(want < cap ? want : cap);
+  const int page_vecs = page_size * row_bytes / 16;
+  const int ctas =
+      table_ctas + (k_pool ? copy_ctas(num_pages / 2, page_vecs) : 0);
+  if (ctas == 0) return cudaSuccess;
+  return launch_kernel<pool_compact_move_kernel>(
+      dim3(ctas), 256, 0, true, stream, bt, mb, ctx, num_seqs, page_size,
+      table_ctas, (const int32_t*)move_src, (const int32_t*)move_dst,
+      (const int32_t*)num_moves, static_cast<uint4*>(k_pool),
+      static_cast<uint4*>(v_pool), num_pages, page_vecs, err);
 }
 
 cudaError_t launch_page_copy(void* k_pool, void* v_pool, int num_pages,
@@ -632,13 +729,8 @@ cudaError_t launch_page_copy(void* k_pool, void* v_pool, int num_pages,
                              const int32_t* num_pairs, uint32_t* err,
                              cudaStream_t stream) {
   if (max_pairs == 0) return cudaSuccess;
-  int dev = 0, sms = 148;
-  cudaGetDevice(&dev);
-  cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
   const int page_vecs = page_bytes / 16;
-  const int64_t want = max_pairs * 2 * ((page_vecs + 1023) / 1024);
-  const int64_t cap = (int64_t)sms * 8;
-  page_copy_kernel<<<(int)(want < cap ? want : cap), 256, 0, stream>>>(
+  page_copy_kernel<<<copy_ctas(max_pairs, page_vecs), 256, 0, stream>>>(
       static_cast<uint4*>(k_pool), static_cast<uint4*>(v_pool), num_pages,
       page_vecs, src, dst, max_pairs, num_pairs, err);
   return cudaGetLastError();

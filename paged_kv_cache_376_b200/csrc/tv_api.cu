@@ -249,14 +249,7 @@ struct BalancedWorkspace {
   size_t bytes;
 };
 
-static int device_sms() {
-  int dev = 0, sms = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess) return 0;
-  if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) !=
-      cudaSuccess)
-    return 0;
-  return sms;
-}
+static int device_sms() { return tv::device_sm_count(); }
 
 static size_t counters_bytes(int num_seqs, int num_kv_heads) {
   return ((size_t)num_seqs * num_kv_heads * 4 + 255) / 256 * 256;

@@ -107,6 +107,16 @@ __device__ __forceinline__ unsigned long long global_timer_ns() {
   return t;
 }
 
+// ---- programmatic dependent launch -------------------------------------------
+// Lets a kernel launched to overlap this one start; and the other side: waits
+// until the kernels before this one have ended and their writes are visible.
+__device__ __forceinline__ void let_next_kernel_start() {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+__device__ __forceinline__ void wait_for_last_kernel() {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+
 // ---- shared-memory addresses ----------------------------------------------
 __device__ __forceinline__ uint32_t smem_u32(const void* p) {
   return static_cast<uint32_t>(__cvta_generic_to_shared(p));

@@ -1,12 +1,61 @@
 // Internal launch interface between the C ABI (tv_api.cu) and the kernels.
 #pragma once
 
+#include <atomic>
 #include <cstdint>
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
 namespace tv {
+
+// SMs of the current device (asked for once per device).
+inline int device_sm_count() {
+  static std::atomic<int> known[64];
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return 0;
+  if (dev < 64 && known[dev].load(std::memory_order_relaxed))
+    return known[dev].load(std::memory_order_relaxed);
+  int sms = 0;
+  if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) !=
+      cudaSuccess)
+    return 0;
+  if (dev < 64) known[dev].store(sms, std::memory_order_relaxed);
+  return sms;
+}
+
+// Launch with `bytes` of dynamic shared memory (the kernel's limit is raised
+// once per device).  With `overlap` the grid may start before the stream's last
+// kernel has ended (programmatic dependent launch); it waits for it with
+// wait_for_last_kernel() (tv_device.cuh).
+template <auto kKernel, typename... Args>
+cudaError_t launch_kernel(dim3 grid, int threads, int bytes, bool overlap,
+                          cudaStream_t stream, Args... args) {
+  static std::atomic<uint64_t> raised;
+  if (bytes > 48 * 1024) {
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    const uint64_t bit = dev < 64 ? 1ull << dev : 0;
+    if (!(raised.load(std::memory_order_relaxed) & bit)) {
+      e = cudaFuncSetAttribute(
+          kKernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+      if (e != cudaSuccess) return e;
+      raised.fetch_or(bit, std::memory_order_relaxed);
+    }
+  }
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = bytes;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr{};
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = overlap ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, kKernel, args...);
+}
 
 struct DecodeArgs {
   __nv_bfloat16* out;            // [B][Hq][D]            (unsplit)

@@ -270,12 +270,16 @@ def test_bindings_refuse_host_tensors_and_shapes():
         _lib.tv_kv_append_mrope(None, q, q, q, i, i, i, pool, pool, q)
 
 
-def test_launch_guard_refuses_mixed_devices():
+def test_one_device_refuses_mixed_devices():
     class T:
-        def __init__(self, dev):
-            self.device = torch.device(dev)
+        def __init__(self, index):
+            self.index = index
+            self.device = torch.device("cuda", index)
+
+        def get_device(self):
+            return self.index
 
     with pytest.raises(ValueError, match="in one call"):
-        _lib._launch(None, T("cuda:0"), None, T("cuda:1"))
+        _lib._one_device((T(0), None, T(1)), None)
     with pytest.raises(ValueError, match="stream on"):
-        _lib._launch(T("cuda:1"), T("cuda:0"))
+        _lib._one_device((T(0),), T(1))
