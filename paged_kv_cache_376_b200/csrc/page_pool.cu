@@ -392,30 +392,69 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (threadIdx.x == 0) *p.top = min(top + base, p.num_pages);
 }
 
+// ---- bitmaps of pages -----------------------------------------------------------
+// Lists the set bits of words w0 .. w0 + nw - 1 in ascending order: emit(i, page)
+// for the i-th, counted from `first`; returns the count behind the last.  One
+// CTA of kThreads; a warp writes a word's pages side by side (one thread per
+// word would scatter a CTA's stores over 32 lines each: 45 us instead of 4 for
+// 18,000 pages).
+constexpr int kWordChunk = 2 * kThreads;
+struct BitList {
+  uint32_t bits[kWordChunk];
+  int base[kWordChunk];
+  int sh[33];
+};
+template <typename Word, typename Emit>
+__device__ __forceinline__ int list_bits(BitList& m, int words, int first,
+                                         Word word, Emit emit) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  for (int c0 = 0; c0 < words; c0 += kWordChunk) {
+    const int w = c0 + 2 * threadIdx.x;
+    const uint32_t b0 = w < words ? word(w) : 0u;
+    const uint32_t b1 = w + 1 < words ? word(w + 1) : 0u;
+    int total;
+    const int pos = first + block_exclusive_scan(__popc(b0) + __popc(b1), m.sh,
+                                                 &total);
+    m.bits[2 * threadIdx.x] = b0;
+    m.bits[2 * threadIdx.x + 1] = b1;
+    m.base[2 * threadIdx.x] = pos;
+    m.base[2 * threadIdx.x + 1] = pos + __popc(b0);
+    __syncthreads();
+    const int nw = min(kWordChunk, words - c0);
+#pragma unroll 4
+    for (int i = warp; i < nw; i += kThreads / 32) {
+      const uint32_t b = m.bits[i];
+      if ((b >> lane) & 1u)
+        emit(m.base[i] + __popc(b & ((1u << lane) - 1)), 32 * (c0 + i) + lane);
+    }
+    first += total;
+    __syncthreads();
+  }
+  return first;
+}
+
 // ---- truncate -----------------------------------------------------------------
 // Sequence s keeps its first new_lens[s] tokens: the pages behind them lose a
 // reference, and those that nobody holds any more go back on the stack in
 // ascending id order, as in a release.
 //
-// Bound: latency (a few integers per dropped page; chains of context -> entry
-// -> count -> mark).  16 lanes per sequence, four pages of each in flight, 64
-// sequences a CTA; the freed pages are marked in a bitmap (one bit per page, in
-// scratch words), whose order is the id order, so a scan over num_pages / 32
-// words by the CTA that ends last replaces a sort.  1024 sequences that drop
-// half of up to 256 pages: one CTA 68 us, this 13 us.
+// Bound: latency (a few integers per dropped page; a chain of context -> entry
+// -> count -> mark).  16 lanes per sequence, eight pages of each in flight; the
+// freed pages are marked in a bitmap (one bit per page, in scratch words),
+// whose order is the id order, so a scan over num_pages / 32 words by the CTA
+// that ends last replaces a sort.
 constexpr int kSeqLanes = 16;
-constexpr int kSeqsPerCta = kThreads / kSeqLanes;
 
 __global__ void __launch_bounds__(kThreads, 1)
     pool_truncate_kernel(PoolView p, int32_t* bt, int mb, int32_t* ctx,
                          const int32_t* new_lens, int num_seqs,
                          uint32_t* err) {
-  __shared__ int sh[33];
+  __shared__ BitList list;
   __shared__ bool last_cta;
   const int kPS = *p.page_size;
   const int top0 = *p.top;
   const int lane = threadIdx.x % kSeqLanes;
-  const int s = blockIdx.x * kSeqsPerCta + threadIdx.x / kSeqLanes;
+  const int s = (blockIdx.x * blockDim.x + threadIdx.x) / kSeqLanes;
   uint32_t* marks = reinterpret_cast<uint32_t*>(p.cnt_app);
   int c = 0, n = 0;
   if (s < num_seqs) {
@@ -430,7 +469,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (s < num_seqs && c >= 0) {
     int32_t* row = bt + (size_t)s * mb;
     const int end = pages_for(c, kPS);
-    constexpr int kU = 4;
+    constexpr int kU = 8;
     for (int k0 = pages_for(n, kPS) + lane; k0 < end; k0 += kU * kSeqLanes) {
       int page[kU], left[kU];
 #pragma unroll
@@ -467,23 +506,18 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncthreads();
     if (!last_cta) return;
   }
-  const int words = (p.num_pages + 31) / 32;
-  int top = top0;
-  for (int w0 = 0; w0 < words; w0 += kThreads) {
-    const int w = w0 + threadIdx.x;
-    uint32_t bits = w < words ? __ldcg(marks + w) : 0u;
-    int tot;
-    int pos = top + block_exclusive_scan(__popc(bits), sh, &tot);
-    if (bits) marks[w] = 0;
-    for (; bits; bits &= bits - 1, ++pos) {
-      // a consistent pool never overflows; a corrupted one is flagged
-      if (pos < p.num_pages)
-        p.stack[pos] = 32 * w + __ffs(bits) - 1;
-      else
-        flag_error(err, DEVERR_BAD_SEQ);
-    }
-    top += tot;
-  }
+  const int top = list_bits(
+      list, (p.num_pages + 31) / 32, top0,
+      [&](int w) {
+        const uint32_t b = __ldcg(marks + w);
+        if (b) marks[w] = 0;
+        return b;
+      },
+      [&](int pos, int page) {
+        // a consistent pool never overflows; a corrupted one is flagged
+        if (pos < p.num_pages) p.stack[pos] = page;
+        else flag_error(err, DEVERR_BAD_SEQ);
+      });
   if (threadIdx.x == 0) *p.top = min(top, p.num_pages);
 }
 
@@ -500,7 +534,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     pool_compact_plan_kernel(PoolView p, int page_size, int32_t* move_src,
                              int32_t* move_dst, int32_t* num_moves,
                              uint32_t* err) {
-  __shared__ int sh[33];
+  __shared__ BitList list;
   __shared__ uint32_t sh_held[kHeldWords];
   let_next_kernel_start();
   const int n = p.num_pages;
@@ -535,28 +569,23 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   }
   int used;
-  (void)block_exclusive_scan(mine, sh, &used);   // its barriers order `held`
-  int ns = 0, nd = 0;
-  for (int w0 = 0; w0 < words; w0 += kThreads) {
-    const int w = w0 + threadIdx.x;
-    uint32_t src = 0, dst = 0;
-    if (w < words) {
-      const uint32_t b = held[w];
-      if (!on_chip) held[w] = 0;
-      // bits of this word whose page id is below `used`
-      const int k = used - 32 * w;
-      const uint32_t low = k >= 32 ? 0xffffffffu : k <= 0 ? 0u : (1u << k) - 1;
-      src = b & ~low;
-      dst = ~b & low;
-    }
-    int ts, td;
-    int ps = ns + block_exclusive_scan(__popc(src), sh, &ts);
-    int pd = nd + block_exclusive_scan(__popc(dst), sh, &td);
-    for (; src; src &= src - 1) move_src[ps++] = 32 * w + __ffs(src) - 1;
-    for (; dst; dst &= dst - 1) move_dst[pd++] = 32 * w + __ffs(dst) - 1;
-    ns += ts;
-    nd += td;
-  }
+  (void)block_exclusive_scan(mine, list.sh, &used);   // its barriers order `held`
+  // bits of word w whose page id is below `used`
+  auto low = [&](int w) {
+    const int k = used - 32 * w;
+    return k >= 32 ? 0xffffffffu : k <= 0 ? 0u : (1u << k) - 1;
+  };
+  const int ns = list_bits(
+      list, words, 0, [&](int w) { return held[w] & ~low(w); },
+      [&](int i, int page) { move_src[i] = page; });
+  list_bits(
+      list, words, 0,
+      [&](int w) {
+        const uint32_t b = held[w];
+        if (!on_chip) held[w] = 0;   // scratch goes back to zero
+        return ~b & low(w);
+      },
+      [&](int i, int page) { move_dst[i] = page; });
   __syncthreads();
   for (int i = threadIdx.x; i < ns; i += kThreads) {
     const int a = move_src[i], b = move_dst[i];
@@ -693,9 +722,9 @@ cudaError_t launch_pool_truncate(int32_t* state, int num_pages, int32_t* bt,
                                  int mb, int32_t* ctx, const int32_t* new_lens,
                                  int num_seqs, uint32_t* err,
                                  cudaStream_t stream) {
-  pool_truncate_kernel<<<(num_seqs + kSeqsPerCta - 1) / kSeqsPerCta, kThreads,
-                         0, stream>>>(view(state, num_pages), bt, mb, ctx,
-                                      new_lens, num_seqs, err);
+  constexpr int per = kThreads / kSeqLanes;
+  pool_truncate_kernel<<<(num_seqs + per - 1) / per, kThreads, 0, stream>>>(
+      view(state, num_pages), bt, mb, ctx, new_lens, num_seqs, err);
   return cudaGetLastError();
 }
 

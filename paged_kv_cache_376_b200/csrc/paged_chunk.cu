@@ -19,9 +19,12 @@
 // O += P V with m16n8k16 bf16 products and fp32 accumulators: with at least
 // 16 rows, rows in the M dimension put P's accumulator fragment where the
 // next product wants its A operand, so P needs no shuffles (the decode
-// kernels, with at most 8 rows, put tokens in M instead).  P enters as two
-// bf16 terms, as in the decode and the prefill, because one term's 8 bits
-// are too few for rows that see few keys.
+// kernels, with at most 8 rows, put tokens in M instead).
+//
+// P enters the second product in bf16.  A weight's rounding (2^-9 of it)
+// averages out over the keys of a row, except where there are few: blocks
+// whose first row sees fewer than kChunkExactKeys keys add P's remainder,
+// P - bf16(P), with a second product, as the decode and the prefill always do.
 #include "tv_decode.cuh"
 #include "tv_device.cuh"
 #include "tv_kernels.h"
@@ -38,6 +41,7 @@ constexpr int kRowBytes = kD * 2;
 constexpr int kSliceBytes = kPS * kRowBytes;
 constexpr int kStageBytes = 2 * kSliceBytes;
 constexpr float kLazy = 8.f;     // log2 of the growth the running sums allow
+constexpr int kExactKeys = kChunkExactKeys;
 
 struct ChunkRing {
   alignas(1024) uint8_t slot[kWarps][kStages][kStageBytes];
@@ -159,6 +163,7 @@ struct WarpRows {
                                        const uint32_t (&voff)[4], float sl,
                                        int lane) {
     const int c = lane & 3;
+    const bool exact = w.first_limit + 1 < kExactKeys;
     uint8_t* vbase = kbase + kSliceBytes;
     // warp-uniform: every row sees every token of the page
     const bool full_page = page_ok && tok0 + kPS - 1 <= w.first_limit;
@@ -242,7 +247,8 @@ struct WarpRows {
           }
         }
     }
-    // P as two bf16 terms (hi + lo, ~16 bits), already in A-operand order
+    // P in bf16 (already in A-operand order), its remainder with it where a row
+    // sees few keys
     uint32_t ph[MB][4], pl[MB][4];
 #pragma unroll
     for (int b = 0; b < MB; ++b)
@@ -256,7 +262,8 @@ struct WarpRows {
           l[b][e] += p0 + p1;
           const uint32_t h = pack_bf16x2(p0, p1);
           ph[b][2 * n + e] = h;
-          pl[b][2 * n + e] = pack_bf16x2(p0 - bf16_lo(h), p1 - bf16_hi(h));
+          if (exact)
+            pl[b][2 * n + e] = pack_bf16x2(p0 - bf16_lo(h), p1 - bf16_hi(h));
         }
       }
 
@@ -269,8 +276,10 @@ struct WarpRows {
       for (int b = 0; b < MB; ++b) {
         mma_bf16_16816(acc[b][2 * t], ph[b], vf[0], vf[1]);
         mma_bf16_16816(acc[b][2 * t + 1], ph[b], vf[2], vf[3]);
-        mma_bf16_16816(acc[b][2 * t], pl[b], vf[0], vf[1]);
-        mma_bf16_16816(acc[b][2 * t + 1], pl[b], vf[2], vf[3]);
+        if (exact) {
+          mma_bf16_16816(acc[b][2 * t], pl[b], vf[0], vf[1]);
+          mma_bf16_16816(acc[b][2 * t + 1], pl[b], vf[2], vf[3]);
+        }
       }
     }
   }
@@ -623,7 +632,6 @@ __global__ void __launch_bounds__(kThreads, 3)
   const int NG = min((int)gridDim.x / Hkv, max(W / kMinChunkBlocks, sm.items));
   const int grp = blockIdx.x / Hkv;
   const int head = blockIdx.x - grp * Hkv;
-  if (grp >= NG) return;
   auto seq_of = [&](int x) {   // pre[s] <= x < pre[s + 1]
     int lo = 0, hi = B;
     while (hi - lo > 1) {
@@ -640,8 +648,12 @@ __global__ void __launch_bounds__(kThreads, 3)
     return y;
   };
   auto raw_cut = [&](int g) { return (int)((int64_t)g * W / NG); };
-  const int x0 = cut(raw_cut(grp)), x1 = cut(raw_cut(grp + 1));
-  if (x0 >= x1) return;
+  const int x0 = grp < NG ? cut(raw_cut(grp)) : 0;
+  const int x1 = grp < NG ? cut(raw_cut(grp + 1)) : 0;
+  if (x0 >= x1) {
+    if (a.tile_ctas) wait_for_last_kernel();
+    return;
+  }
 
   // ---- the warp's blocks: x0 + warp + 4 i --------------------------------------------
   const int my_n =
@@ -802,34 +814,25 @@ __global__ void __launch_bounds__(kThreads, 3)
     for (int k = i; k < issued; ++k)
       mbar_wait(smem_u32(&sm.ring.full[warp][k % kStages]), (k / kStages) & 1);
   }
+  // the rows of the tile kernel are written when this kernel ends
+  if (a.tile_ctas) wait_for_last_kernel();
 }
 
 static_assert(3 * (sizeof(BalancedSmem) + 1024 + 1024) <= 228 * 1024,
               "three CTAs must fit in an SM's shared memory");
 
-template <typename Kernel>
-cudaError_t launch_with(Kernel kern, dim3 grid, int smem, const ChunkArgs& a,
-                        const CUtensorMap& tk, const CUtensorMap& tv,
-                        cudaStream_t stream) {
-  cudaError_t e = cudaFuncSetAttribute(
-      kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-  if (e != cudaSuccess) return e;
-  kern<<<grid, kThreads, smem, stream>>>(a, tk, tv);
-  return cudaGetLastError();
-}
-
 template <int MB, bool kCausal>
 cudaError_t launch_mb(const ChunkArgs& a, const CUtensorMap& tk,
                       const CUtensorMap& tv, cudaStream_t stream) {
+  // behind the tile kernel it fills the SMs that run out of tiles
   if (a.balanced_ctas)
-    return launch_with(balanced_chunk_kernel<MB, kCausal>,
-                       dim3(a.balanced_ctas), sizeof(BalancedSmem) + 1024, a,
-                       tk, tv, stream);
+    return launch_kernel<balanced_chunk_kernel<MB, kCausal>>(
+        dim3(a.balanced_ctas), kThreads, sizeof(BalancedSmem) + 1024,
+        a.tile_ctas > 0, stream, a, tk, tv);
   const int per = (16 * MB) >> a.group_shift;
-  return launch_with(paged_chunk_kernel<MB, kCausal>,
-                     dim3(a.num_kv_heads, a.num_seqs,
-                          (a.max_query_len + per - 1) / per),
-                     sizeof(ChunkRing) + 1024, a, tk, tv, stream);
+  return launch_kernel<paged_chunk_kernel<MB, kCausal>>(
+      dim3(a.num_kv_heads, a.num_seqs, (a.max_query_len + per - 1) / per),
+      kThreads, sizeof(ChunkRing) + 1024, false, stream, a, tk, tv);
 }
 
 }  // namespace

@@ -68,7 +68,7 @@ constexpr int kSCol = 0;                  // S, then P, in buffer b of query
                                           // tile t: [64 (3 t + b), +64)
 constexpr int kOCol = 384;                // O of tile t: [384 + 64 t, +64)
 constexpr float kLazy = 8.f;              // log2 of the growth allowed
-constexpr int kExactKeys = 512;           // see the file comment
+constexpr int kExactKeys = kChunkExactKeys;   // see the file comment
 constexpr int kMinTiles = 4;              // key tiles worth a unit of their own
 
 constexpr uint32_t kIdescQK = idesc_bf16_f32(kBM, kHalf, false);
@@ -105,8 +105,7 @@ __device__ __forceinline__ bool tile_block(const ChunkArgs& a, int seq,
 }
 
 constexpr int kPlanThreads = 1024;
-constexpr int kBuckets = 4096;            // costs above share the top
-constexpr int kPerThread = kBuckets / kPlanThreads;
+constexpr int kBuckets = kPlanThreads;     // costs above share the top
 
 template <bool kCausal>
 __global__ void __launch_bounds__(kPlanThreads, 1)
@@ -115,23 +114,34 @@ __global__ void __launch_bounds__(kPlanThreads, 1)
   __shared__ int warp_sum[32];
   __shared__ unsigned long long total;
   __shared__ int parts;
+  let_next_kernel_start();
   const int nblk = chunk_tile_blocks(a.max_query_len, a.group_shift);
   const int n_items = a.num_seqs * nblk;
-  for (int i = threadIdx.x; i < kBuckets; i += kPlanThreads) slot[i] = 0;
+  slot[threadIdx.x] = 0;
   if (threadIdx.x == 0) {
     total = 0;
     parts = 0;
   }
-  __syncthreads();
   auto tiles_of = [&](int item, Block* b) {
     return tile_block<kCausal>(a, item / nblk, item % nblk, b)
                ? (b->key_end + kBN - 1) / kBN
                : -1;
   };
+  // the thread's first item stays in registers for the further passes
+  Block b0{};
+  const int n0 = (int)threadIdx.x < n_items ? tiles_of(threadIdx.x, &b0) : -1;
+  auto again = [&](int item, Block* b) {
+    if (item == (int)threadIdx.x) {
+      *b = b0;
+      return n0;
+    }
+    return tiles_of(item, b);
+  };
   Block b;
-  long long mine = 0;
-  for (int i = threadIdx.x; i < n_items; i += kPlanThreads)
+  long long mine = max(0, n0);
+  for (int i = threadIdx.x + kPlanThreads; i < n_items; i += kPlanThreads)
     mine += max(0, tiles_of(i, &b));
+  __syncthreads();
   if (mine) atomicAdd(&total, (unsigned long long)mine);
   __syncthreads();
   // no unit longer than half an SM's share, none shorter than kMinTiles
@@ -149,21 +159,15 @@ __global__ void __launch_bounds__(kPlanThreads, 1)
   };
   auto edge = [](int n, int k, int of) { return (int)((long long)n * k / of); };
   for (int i = threadIdx.x; i < n_items; i += kPlanThreads) {
-    const int n = tiles_of(i, &b);
+    const int n = again(i, &b);
     if (n < 0) continue;
     const int of = cuts_of(n);
     for (int k = 0; k < of; ++k)
       atomicAdd(&slot[cost(b, edge(n, k + 1, of) - edge(n, k, of))], 1);
   }
   __syncthreads();
-  // thread t owns the costs kBuckets-1-4t down to ...-4t-3
-  int own[kPerThread];
-  int sum = 0;
-#pragma unroll
-  for (int k = 0; k < kPerThread; ++k) {
-    own[k] = slot[kBuckets - 1 - (threadIdx.x * kPerThread + k)];
-    sum += own[k];
-  }
+  // thread t owns the cost kBuckets - 1 - t
+  const int sum = slot[kBuckets - 1 - threadIdx.x];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   int incl = sum;
 #pragma unroll
@@ -183,19 +187,15 @@ __global__ void __launch_bounds__(kPlanThreads, 1)
     warp_sum[lane] = w;
   }
   __syncthreads();
-  int start = incl - sum + (warp > 0 ? warp_sum[warp - 1] : 0);
-#pragma unroll
-  for (int k = 0; k < kPerThread; ++k) {
-    slot[kBuckets - 1 - (threadIdx.x * kPerThread + k)] = start;
-    start += own[k];
-  }
+  const int start = incl - sum + (warp > 0 ? warp_sum[warp - 1] : 0);
+  slot[kBuckets - 1 - threadIdx.x] = start;
   if (threadIdx.x == kPlanThreads - 1) {
-    a.plan->entries = start;
+    a.plan->entries = start + sum;
     a.plan->next = a.tile_ctas;
   }
   __syncthreads();
   for (int i = threadIdx.x; i < n_items; i += kPlanThreads) {
-    const int n = tiles_of(i, &b);
+    const int n = again(i, &b);
     if (n < 0) continue;
     const int of = cuts_of(n);
     const int base = of > 1 ? atomicAdd(&parts, of) : -1;
@@ -267,7 +267,10 @@ __device__ __forceinline__ void unit_at(const ChunkArgs& a, int i, int n_units,
   u->live = i < n_units;
   u->n_tiles = 0;
   if (!u->live) return;
-  u->e = a.plan_entries[i / a.num_kv_heads];
+  const int4* e =
+      reinterpret_cast<const int4*>(a.plan_entries + i / a.num_kv_heads);
+  const int4 e0 = __ldcg(e), e1 = __ldcg(e + 1);
+  u->e = ChunkEntry{e0.x, e0.y, e0.z, e0.w, e1.x, e1.y, e1.z, e1.w};
   u->kvh = i % a.num_kv_heads;
   tile_block<kCausal>(a, u->e.seq, u->e.blk, &u->b);
   const int per = kBM >> a.group_shift;
@@ -441,8 +444,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   auto& sm = *reinterpret_cast<TileSmem*>(base);
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
-  const int n_units = a.plan->entries * a.num_kv_heads;
-  if ((int)blockIdx.x >= n_units) return;
+  let_next_kernel_start();
   const int per = kBM >> a.group_shift;     // query rows of a tile
 
   if (threadIdx.x == 0) {
@@ -476,6 +478,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = sm.tmem_base;
+  wait_for_last_kernel();                   // the plan
+  const int n_units = __ldcg(&a.plan->entries) * a.num_kv_heads;
 
   // `it` counts the K/V tiles of all units of the CTA, a Turn the halves of a
   // query tile.  A barrier's n-th use (from 0) completes its phase of parity
@@ -1009,16 +1013,12 @@ template <bool kCausal>
 cudaError_t launch(const ChunkArgs& a, const CUtensorMap& tq,
                    const CUtensorMap& tk, const CUtensorMap& tv,
                    cudaStream_t stream) {
-  const int smem = sizeof(TileSmem) + 1024;
-  auto kern = chunk_tile_kernel<kCausal>;
-  cudaError_t e = cudaFuncSetAttribute(
-      kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  cudaError_t e = launch_kernel<chunk_plan_kernel<kCausal>>(
+      dim3(1), kPlanThreads, 0, false, stream, a);
   if (e != cudaSuccess) return e;
-  chunk_plan_kernel<kCausal><<<1, kPlanThreads, 0, stream>>>(a);
-  e = cudaGetLastError();
-  if (e != cudaSuccess) return e;
-  kern<<<a.tile_ctas, kThreads, smem, stream>>>(a, tq, tk, tv);
-  return cudaGetLastError();
+  return launch_kernel<chunk_tile_kernel<kCausal>>(
+      dim3(a.tile_ctas), kThreads, sizeof(TileSmem) + 1024, true, stream, a,
+      tq, tk, tv);
 }
 
 }  // namespace
