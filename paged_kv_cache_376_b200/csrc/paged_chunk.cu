@@ -43,17 +43,20 @@ constexpr int kStageBytes = 2 * kSliceBytes;
 constexpr float kLazy = 8.f;     // log2 of the growth the running sums allow
 constexpr int kExactKeys = kChunkExactKeys;
 
+template <int kW>
 struct ChunkRing {
-  alignas(1024) uint8_t slot[kWarps][kStages][kStageBytes];
-  alignas(8) uint64_t full[kWarps][kStages];
+  alignas(1024) uint8_t slot[kW][kStages][kStageBytes];
+  alignas(8) uint64_t full[kW][kStages];
+  uint64_t empty[kW][kStages];
 };
 
 // Per-warp results of 16 rows, handed to the combine (rows padded so that the
 // lanes of a fragment hit different banks).
+template <int kW>
 struct ChunkCombine {
-  float m[kWarps][16];
-  float l[kWarps][16];
-  alignas(16) float acc[kWarps][16][kD + 8];
+  float m[kW][16];
+  float l[kW][16];
+  alignas(16) float acc[kW][16][kD + 8];
 };
 
 // The rows of one sequence that a CTA works on, and the keys they see.
@@ -156,8 +159,9 @@ struct WarpRows {
       }
   }
 
-  // One 16-token page that lies in a ring slot: tokens tok0 .. tok0 + 15.
-  __device__ __forceinline__ void page(uint8_t* kbase, int tok0, bool page_ok,
+  // One 16-token page that lies in a ring slot: tokens tok0 .. tok0 + 15.  True
+  // when it wrote into the slot.
+  __device__ __forceinline__ bool page(uint8_t* kbase, int tok0, bool page_ok,
                                        const ChunkRows& w,
                                        const uint32_t (&koff)[4],
                                        const uint32_t (&voff)[4], float sl,
@@ -201,71 +205,78 @@ struct WarpRows {
         mma_bf16_16816(s[b][1], qa[b][k], kf[2], kf[3]);
       }
     }
-    if (!full_page) {
-#pragma unroll
-      for (int b = 0; b < MB; ++b)
-#pragma unroll
-        for (int n = 0; n < 2; ++n)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const int tok = tok0 + 8 * n + 2 * c + (e & 1);
-            if (!(page_ok && tok <= limit[b][e >> 1])) s[b][n][e] = -INFINITY;
-          }
-    }
-
-    // ---- online softmax; the offset moves only when a page's maximum exceeds
-    //      it by 2^kLazy (any offset gives the same acc / l) ------------------
-    float pm[MB][2];
-    bool grow = false;
+    // ---- weights against the offsets as they stand, in bf16 and already in
+    //      A-operand order.  Where a score exceeds its row's offset by 2^kLazy
+    //      (any offset gives the same acc / l), and on pages with hidden
+    //      tokens, the row's maximum is taken, its offset moved and the
+    //      weights are done again; the check is off the path to the
+    //      exponentials, and needs no exchange between lanes -----------------
+    uint32_t ph[MB][4];
+    auto weight = [&](int b, int n, int e, int k) {
+      const float mu = m[b][e] == -INFINITY ? 0.f : m[b][e];
+      return fast_exp2(fmaf(s[b][n][2 * e + k], sl, -mu));
+    };
+    float top = -INFINITY, ls[MB][2];
 #pragma unroll
     for (int b = 0; b < MB; ++b)
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
-        float x = fmaxf(fmaxf(s[b][0][2 * e], s[b][0][2 * e + 1]),
-                        fmaxf(s[b][1][2 * e], s[b][1][2 * e + 1]));
-        x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 1));
-        x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 2));
-        pm[b][e] = x * sl;          // scale > 0: the maximum commutes with it
-        grow |= pm[b][e] > m[b][e] + kLazy;
+        ls[b][e] = 0.f;
+#pragma unroll
+        for (int n = 0; n < 2; ++n) {
+          // (an offset of -inf, no key seen yet, makes x +inf: done again)
+          const float x0 = fmaf(s[b][n][2 * e], sl, -m[b][e]);
+          const float x1 = fmaf(s[b][n][2 * e + 1], sl, -m[b][e]);
+          top = fmax3(top, x0, x1);
+          const float p0 = fast_exp2(x0), p1 = fast_exp2(x1);
+          ls[b][e] += p0 + p1;
+          ph[b][2 * n + e] = pack_bf16x2(p0, p1);
+        }
       }
-    if (__any_sync(0xffffffffu, grow)) {
+    if (!full_page || __any_sync(0xffffffffu, top > kLazy)) {
 #pragma unroll
       for (int b = 0; b < MB; ++b)
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
+          float x = -INFINITY;
+#pragma unroll
+          for (int n = 0; n < 2; ++n)
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+              const int tok = tok0 + 8 * n + 2 * c + k;
+              if (!(page_ok && tok <= limit[b][e]))
+                s[b][n][2 * e + k] = -INFINITY;
+              x = fmaxf(x, s[b][n][2 * e + k]);
+            }
+          x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 1));
+          x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 2));
+          x *= sl;                    // scale > 0: the maximum commutes with it
           // a row's offset depends on its own scores alone, so a row gives
           // the same result whatever stands in the rows beside it
-          if (!(pm[b][e] > m[b][e] + kLazy)) continue;
-          const float n = pm[b][e];
-          const float f = fast_exp2(m[b][e] - n);
-          m[b][e] = n;
-          l[b][e] *= f;
+          if (x > m[b][e] + kLazy) {
+            const float f = fast_exp2(m[b][e] - x);
+            m[b][e] = x;
+            l[b][e] *= f;
 #pragma unroll
-          for (int d = 0; d < 8; ++d) {
-            acc[b][d][2 * e] *= f;
-            acc[b][d][2 * e + 1] *= f;
+            for (int d = 0; d < 8; ++d) {
+              acc[b][d][2 * e] *= f;
+              acc[b][d][2 * e + 1] *= f;
+            }
+          }
+          ls[b][e] = 0.f;
+#pragma unroll
+          for (int n = 0; n < 2; ++n) {
+            const float p0 = weight(b, n, e, 0), p1 = weight(b, n, e, 1);
+            ls[b][e] += p0 + p1;
+            ph[b][2 * n + e] = pack_bf16x2(p0, p1);
           }
         }
     }
-    // P in bf16 (already in A-operand order), its remainder with it where a row
-    // sees few keys
-    uint32_t ph[MB][4], pl[MB][4];
 #pragma unroll
-    for (int b = 0; b < MB; ++b)
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        const float mu = m[b][e] == -INFINITY ? 0.f : m[b][e];
-#pragma unroll
-        for (int n = 0; n < 2; ++n) {
-          const float p0 = fast_exp2(fmaf(s[b][n][2 * e], sl, -mu));
-          const float p1 = fast_exp2(fmaf(s[b][n][2 * e + 1], sl, -mu));
-          l[b][e] += p0 + p1;
-          const uint32_t h = pack_bf16x2(p0, p1);
-          ph[b][2 * n + e] = h;
-          if (exact)
-            pl[b][2 * n + e] = pack_bf16x2(p0 - bf16_lo(h), p1 - bf16_hi(h));
-        }
-      }
+    for (int b = 0; b < MB; ++b) {
+      l[b][0] += ls[b][0];
+      l[b][1] += ls[b][1];
+    }
 
     // ---- O += P V --------------------------------------------------------------
 #pragma unroll
@@ -276,12 +287,31 @@ struct WarpRows {
       for (int b = 0; b < MB; ++b) {
         mma_bf16_16816(acc[b][2 * t], ph[b], vf[0], vf[1]);
         mma_bf16_16816(acc[b][2 * t + 1], ph[b], vf[2], vf[3]);
-        if (exact) {
-          mma_bf16_16816(acc[b][2 * t], pl[b], vf[0], vf[1]);
-          mma_bf16_16816(acc[b][2 * t + 1], pl[b], vf[2], vf[3]);
+      }
+    }
+    if (exact) {   // the weights' remainders
+#pragma unroll
+      for (int b = 0; b < MB; ++b)
+#pragma unroll
+        for (int e = 0; e < 2; ++e)
+#pragma unroll
+          for (int n = 0; n < 2; ++n) {
+            const uint32_t h = ph[b][2 * n + e];
+            ph[b][2 * n + e] = pack_bf16x2(weight(b, n, e, 0) - bf16_lo(h),
+                                           weight(b, n, e, 1) - bf16_hi(h));
+          }
+#pragma unroll
+      for (int t = 0; t < 4; ++t) {
+        uint32_t vf[4];
+        ldsm_x4_trans(vb + voff[t], vf);
+#pragma unroll
+        for (int b = 0; b < MB; ++b) {
+          mma_bf16_16816(acc[b][2 * t], ph[b], vf[0], vf[1]);
+          mma_bf16_16816(acc[b][2 * t + 1], ph[b], vf[2], vf[3]);
         }
       }
     }
+    return !full_page;
   }
 
   // The quads hold a row's sum in four parts.
@@ -295,7 +325,8 @@ struct WarpRows {
       }
   }
 
-  __device__ __forceinline__ void put(ChunkCombine& cb, int b, int warp,
+  template <int kW>
+  __device__ __forceinline__ void put(ChunkCombine<kW>& cb, int b, int warp,
                                       int lane) const {
     const int g = lane >> 2, c = lane & 3;
 #pragma unroll
@@ -341,13 +372,14 @@ struct Joined {
   }
 };
 
-__device__ __forceinline__ Joined join_warps(const ChunkCombine& cb, int r,
+template <int kW>
+__device__ __forceinline__ Joined join_warps(const ChunkCombine<kW>& cb, int r,
                                              int k) {
   Joined j;
 #pragma unroll
-  for (int w = 0; w < kWarps; ++w) j.M = fmaxf(j.M, cb.m[w][r]);
+  for (int w = 0; w < kW; ++w) j.M = fmaxf(j.M, cb.m[w][r]);
 #pragma unroll
-  for (int w = 0; w < kWarps; ++w)
+  for (int w = 0; w < kW; ++w)
     j.add(cb.m[w][r], cb.l[w][r],
           *reinterpret_cast<const float4*>(&cb.acc[w][r][4 * k]),
           *reinterpret_cast<const float4*>(&cb.acc[w][r][32 + 4 * k]));
@@ -430,11 +462,11 @@ __global__ void __launch_bounds__(kThreads, 3)
     paged_chunk_kernel(const ChunkArgs a,
                        const __grid_constant__ CUtensorMap tm_k,
                        const __grid_constant__ CUtensorMap tm_v) {
-  static_assert(sizeof(ChunkCombine) <= sizeof(ChunkRing::slot),
+  static_assert(sizeof(ChunkCombine<kWarps>) <= sizeof(ChunkRing<kWarps>::slot),
                 "the combine buffer must fit in the ring");
   extern __shared__ __align__(1024) uint8_t smem_dyn[];
   uint8_t* smem_raw = smem_dyn + ((1024 - (smem_u32(smem_dyn) & 1023)) & 1023);
-  auto& sm = *reinterpret_cast<ChunkRing*>(smem_raw);
+  auto& sm = *reinterpret_cast<ChunkRing<kWarps>*>(smem_raw);
 
   const int kvh = blockIdx.x;
   const int seq = blockIdx.y;
@@ -502,11 +534,11 @@ __global__ void __launch_bounds__(kThreads, 3)
       failed = true;
       break;
     }
-    rows.page(&sm.slot[warp][stage][0], (warp + kWarps * i) * kPS, page_ok, w,
-              koff, voff, a.scale_log2, lane);
-
-    // ---- hand the slot back to the TMA unit ------------------------------------
-    fence_proxy_async_smem();
+    // ---- hand the slot back to the TMA unit (plain writes into it are ordered
+    //      before the copies that follow) -----------------------------------------
+    if (rows.page(&sm.slot[warp][stage][0], (warp + kWarps * i) * kPS, page_ok,
+                  w, koff, voff, a.scale_log2, lane))
+      fence_proxy_async_smem();
     __syncwarp();
     const int j = i + kStages;
     const int src = ((j >> 5) == (i >> 5)) ? cur : next;
@@ -526,7 +558,7 @@ __global__ void __launch_bounds__(kThreads, 3)
 
   // ---- combine the four warps, 16 rows at a time, and write -----------------------
   rows.finish_sums();
-  auto& cb = *reinterpret_cast<ChunkCombine*>(smem_raw);
+  auto& cb = *reinterpret_cast<ChunkCombine<kWarps>*>(smem_raw);
   const int n_rows = w.tb << a.group_shift;
 #pragma unroll
   for (int b = 0; b < MB; ++b) {
@@ -556,27 +588,69 @@ __global__ void __launch_bounds__(kThreads, 3)
 // the ranges (results do not depend on timing), and sets the counter back to
 // zero.  No CTA waits for another.
 //
-// The ring of a warp runs across sequence ends: the loads of the next
-// sequence are in flight while the last one's warps are combined.
+// W warps compute, block x0 + w + W i the i-th of warp w; one more looks the
+// blocks up and issues the loads into their rings.  The rings run across
+// sequence ends: the loads of the next sequence are in flight while the last
+// one's warps are combined.  (With each warp issuing its own loads a block of
+// 32 rows took it 670 of 2370 clocks.)
 constexpr int kSnap = 4;
+// A sub-core's 16,384 registers hold three warps of 32 rows or four of 16 rows
+// without spills: 6 or 7 warps a CTA, two CTAs an SM.
+__host__ __device__ constexpr int compute_warps(int mb) { return mb == 1 ? 6 : 5; }
 
+template <int kW>
 struct BalancedSmem {
-  ChunkRing ring;
-  ChunkCombine cb;
-  int32_t warp_total[kWarps];
+  ChunkRing<kW> ring;
+  ChunkCombine<kW> cb;
+  int32_t warp_total[kW + 1];
   int32_t items;
   int32_t last;
+  uint32_t bad[kW][kStages];   // the slot's block was no page
   int32_t pre[kMaxChunkSeqs + 1];
 };
 
+// The CTA's range of blocks, from the prefix sums in shared memory.
+struct BlockLine {
+  const int32_t* pre;
+  int B, W, NG;
+  __device__ __forceinline__ int seq_of(int x) const {   // pre[s] <= x < pre[s+1]
+    int lo = 0, hi = B;
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (pre[mid] <= x) lo = mid; else hi = mid;
+    }
+    return lo;
+  }
+  __device__ __forceinline__ int raw(int g) const {
+    return W < 1 << 20 ? (int)((uint32_t)g * (uint32_t)W / (uint32_t)NG)
+                       : (int)((int64_t)g * W / NG);
+  }
+  // first block of group g's range: moved to a close sequence end
+  __device__ __forceinline__ int cut(int g) const {
+    const int y = raw(g);
+    if (y >= W) return W;
+    const int s = seq_of(y);
+    if (y - pre[s] < kSnap) return pre[s];
+    if (pre[s + 1] - y < kSnap) return pre[s + 1];
+    return y;
+  }
+};
+
+template <int kW>
+__device__ __forceinline__ void compute_barrier() {
+  asm volatile("bar.sync 1, %0;" ::"n"(kW * 32) : "memory");
+}
+
 template <int MB, bool kCausal>
-__global__ void __launch_bounds__(kThreads, 3)
+__global__ void __launch_bounds__((compute_warps(MB) + 1) * 32, kChunkCtasPerSm)
     balanced_chunk_kernel(const ChunkArgs a,
                           const __grid_constant__ CUtensorMap tm_k,
                           const __grid_constant__ CUtensorMap tm_v) {
+  constexpr int kW = compute_warps(MB);
+  constexpr int kBalancedThreads = (kW + 1) * 32;
   extern __shared__ __align__(1024) uint8_t smem_dyn[];
   uint8_t* smem_raw = smem_dyn + ((1024 - (smem_u32(smem_dyn) & 1023)) & 1023);
-  auto& sm = *reinterpret_cast<BalancedSmem*>(smem_raw);
+  auto& sm = *reinterpret_cast<BalancedSmem<kW>*>(smem_raw);
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
   const int B = a.num_seqs;
@@ -584,242 +658,256 @@ __global__ void __launch_bounds__(kThreads, 3)
 
   // ---- blocks per sequence, exclusive prefix in shared memory ------------------
   if (threadIdx.x == 0) sm.items = 0;
-  __syncthreads();
-  int mine = 0;
-  for (int s = threadIdx.x; s < B; s += kThreads) {
+  if (lane == 0 && warp < kW) {
+    for (int s = 0; s < kStages; ++s) {
+      mbar_init(smem_u32(&sm.ring.full[warp][s]), 1);
+      mbar_init(smem_u32(&sm.ring.empty[warp][s]), 1);
+    }
+    fence_mbar_init();
+  }
+  // thread t sums the sequences t * per .. + per - 1
+  const int per = (B + kBalancedThreads - 1) / kBalancedThreads;
+  const int s0 = min(B, (int)threadIdx.x * per), s1 = min(B, s0 + per);
+  int own = 0, live_seqs = 0;
+  for (int s = s0; s < s1; ++s) {
     int qs, T, ctx;
     const bool live = sequence_rows<kCausal>(a, s, blockIdx.x == 0, &qs, &T,
                                              &ctx) &&
                       T <= a.stream_rows;
     // a sequence without keys keeps one block, not loaded, for its zero rows
-    sm.pre[s] = live ? max(1, (ctx + kPS - 1) / kPS) : 0;
-    mine += live;
+    const int n = live ? max(1, (ctx + kPS - 1) / kPS) : 0;
+    sm.pre[s] = n;
+    own += n;
+    live_seqs += live;
   }
-  if (mine) atomicAdd(&sm.items, mine);
-  __syncthreads();
-  {
-    const int per = (B + kThreads - 1) / kThreads;
-    const int lo = min(B, (int)threadIdx.x * per);
-    const int hi = min(B, lo + per);
-    int own = 0;
-    for (int s = lo; s < hi; ++s) own += sm.pre[s];
-    int incl = own;
+  int incl = own;
 #pragma unroll
-    for (int off = 1; off < 32; off <<= 1) {
-      const int v = __shfl_up_sync(0xffffffffu, incl, off);
-      if (lane >= off) incl += v;
-    }
-    if (lane == 31) sm.warp_total[warp] = incl;
-    __syncthreads();
-    int run = incl - own;
-    for (int v = 0; v < warp; ++v) run += sm.warp_total[v];
-    for (int s = lo; s < hi; ++s) {
-      const int n = sm.pre[s];
-      sm.pre[s] = run;
-      run += n;
-    }
-    if (threadIdx.x == kThreads - 1) sm.pre[B] = run;
+  for (int off = 1; off < 32; off <<= 1) {
+    const int v = __shfl_up_sync(0xffffffffu, incl, off);
+    if (lane >= off) incl += v;
   }
-  if (lane == 0) {
-    for (int s = 0; s < kStages; ++s)
-      mbar_init(smem_u32(&sm.ring.full[warp][s]), 1);
-    fence_mbar_init();
+  if (lane == 31) sm.warp_total[warp] = incl;
+  __syncthreads();
+  if (live_seqs) atomicAdd(&sm.items, live_seqs);
+  int run = incl - own;
+  for (int v = 0; v < warp; ++v) run += sm.warp_total[v];
+  for (int s = s0; s < s1; ++s) {
+    const int n = sm.pre[s];
+    sm.pre[s] = run;
+    run += n;
   }
+  if (threadIdx.x == kBalancedThreads - 1) sm.pre[B] = run;
   __syncthreads();
 
   // ---- this CTA's range ----------------------------------------------------------
-  const int W = sm.pre[B];
-  const int NG = min((int)gridDim.x / Hkv, max(W / kMinChunkBlocks, sm.items));
+  BlockLine line;
+  line.pre = sm.pre;
+  line.B = B;
+  line.W = sm.pre[B];
+  line.NG = min((int)gridDim.x / Hkv, max(line.W / kMinChunkBlocks, sm.items));
+  const int W = line.W, NG = line.NG;
   const int grp = blockIdx.x / Hkv;
   const int head = blockIdx.x - grp * Hkv;
-  auto seq_of = [&](int x) {   // pre[s] <= x < pre[s + 1]
-    int lo = 0, hi = B;
-    while (hi - lo > 1) {
-      const int mid = (lo + hi) >> 1;
-      if (sm.pre[mid] <= x) lo = mid; else hi = mid;
-    }
-    return lo;
-  };
-  auto cut = [&](int y) {      // a range boundary, moved to a close sequence end
-    if (y >= W) return W;
-    const int s = seq_of(y);
-    if (y - sm.pre[s] < kSnap) return sm.pre[s];
-    if (sm.pre[s + 1] - y < kSnap) return sm.pre[s + 1];
-    return y;
-  };
-  auto raw_cut = [&](int g) { return (int)((int64_t)g * W / NG); };
-  const int x0 = grp < NG ? cut(raw_cut(grp)) : 0;
-  const int x1 = grp < NG ? cut(raw_cut(grp + 1)) : 0;
-  if (x0 >= x1) {
-    if (a.tile_ctas) wait_for_last_kernel();
-    return;
-  }
+  const int x0 = grp < NG ? line.cut(grp) : 0;
+  const int x1 = grp < NG ? line.cut(grp + 1) : 0;
+  const int steps = (x1 - x0 + kW - 1) / kW;
 
-  // ---- the warp's blocks: x0 + warp + 4 i --------------------------------------------
-  const int my_n =
-      x1 - x0 > warp ? (x1 - x0 - warp + kWarps - 1) / kWarps : 0;
-  auto load_blocks = [&](int batch) -> int {
-    const int i = batch * 32 + lane;
-    if (i >= my_n) return -1;
-    const int x = x0 + warp + kWarps * i;
-    const int s = seq_of(x);
-    // (a sequence without keys reads an entry of its own row, or none)
-    return a.context_lens[s] > 0 ? pool_block(a, s, x - sm.pre[s]) : 0;
-  };
-  const uint64_t policy = l2_policy_evict_first();
-  auto issue = [&](int block, int stage) {
-    issue_block(a, &tm_k, &tm_v, head * kD, block,
-                smem_u32(&sm.ring.slot[warp][stage][0]),
-                smem_u32(&sm.ring.full[warp][stage]), policy);
-  };
-  int cur = load_blocks(0), next = load_blocks(1);
-#pragma unroll
-  for (int j = 0; j < kStages; ++j) {
-    const int block = __shfl_sync(0xffffffffu, cur, j);
-    if (lane == 0 && j < my_n) issue(block, j);
-  }
-  uint32_t koff[4], voff[4];
-  slice_offsets(lane, koff, voff);
-
-  WarpRows<MB, kCausal> rows;
-  bool failed = false;
-  int issued = min(my_n, kStages);
-  int i = 0;                          // blocks this warp has done
-  int seq = seq_of(x0);
-  int next_qs, next_T, next_ctx;
-  sequence_rows<kCausal>(a, seq, false, &next_qs, &next_T, &next_ctx);
-  for (int p0 = x0; p0 < x1;) {
-    const int base = sm.pre[seq];
-    const int end = min(x1, sm.pre[seq + 1]);
-    const int qs = next_qs, T = next_T, ctx = next_ctx;
-    int next_seq = seq;
-    if (end < x1) {   // the next sequence's rows, and its q into the cache
-      do ++next_seq; while (sm.pre[next_seq + 1] <= end);
-      sequence_rows<kCausal>(a, next_seq, false, &next_qs, &next_T, &next_ctx);
-      if (warp == 0 && lane < next_T << a.group_shift)
-        asm volatile("prefetch.global.L1 [%0];" ::"l"(
-            a.q + ((size_t)(next_qs + (lane >> a.group_shift)) *
-                       a.num_q_heads + (head << a.group_shift) +
-                   (lane & ((1 << a.group_shift) - 1))) * kD));
-    }
-    ChunkRows w;
-    w.q_row = qs;
-    w.tb = T;
-    w.first_limit = kCausal ? ctx - T : ctx - 1;
-    w.key_end = ctx;
-    rows.load(a, w, head, lane);
-    rows.clear();
-    for (; i < my_n && !failed; ++i) {
-      const int x = x0 + warp + kWarps * i;
-      if (x >= end) break;
-      const int stage = i % kStages;
-      if ((i & 31) == 0 && i > 0) {
-        cur = next;
-        next = load_blocks((i >> 5) + 1);
+  if (warp == kW) {
+    // ======================= loads =============================================
+    // Lane 2 w + v issues K (v = 0) or V of warp w's block; the blocks of as many
+    // steps as fit are looked up one per lane.
+    constexpr int kLook = 32 / kW;
+    const int w = lane >> 1;
+    const bool is_v = lane & 1;
+    const bool issuer = lane < 2 * kW;
+    const uint64_t policy = l2_policy_evict_first();
+    const CUtensorMap* tm = is_v ? &tm_v : &tm_k;
+    auto look_up = [&](int step) -> int {
+      const int x = x0 + step * kW + lane;
+      if (lane >= kLook * kW || x >= x1) return -2;
+      const int s = line.seq_of(x);
+      // (a sequence without keys has nothing to look up: block 0)
+      return a.context_lens[s] > 0 ? pool_block(a, s, x - sm.pre[s]) : 0;
+    };
+    int blocks = look_up(0), ahead = look_up(kLook);
+    int in_look = 0;
+    bool ok = true;
+    int i = 0;
+    for (; i < steps; ++i) {
+      if (in_look == kLook) {
+        in_look = 0;
+        blocks = ahead;
+        ahead = look_up(i + kLook);
       }
-      const bool page_ok = __shfl_sync(0xffffffffu, cur, i & 31) >= 0;
-      if (!__all_sync(0xffffffffu,
-                      mbar_wait(smem_u32(&sm.ring.full[warp][stage]),
-                                (i / kStages) & 1))) {
-        failed = true;
+      const int block = __shfl_sync(0xffffffffu, blocks,
+                                    in_look * kW +
+                                        (issuer ? w : 0));
+      ++in_look;
+      const int stage = i % kStages;
+      const bool mine = issuer && block != -2;
+      const bool ready =
+          !mine || i < kStages ||
+          mbar_wait(smem_u32(&sm.ring.empty[w][stage]), (i / kStages + 1) & 1);
+      if (!__all_sync(0xffffffffu, ready)) {
+        ok = false;
         break;
       }
-      rows.page(&sm.ring.slot[warp][stage][0], (x - base) * kPS, page_ok, w,
-                koff, voff, a.scale_log2, lane);
-      fence_proxy_async_smem();
-      __syncwarp();
-      const int j = i + kStages;
-      const int src = ((j >> 5) == (i >> 5)) ? cur : next;
-      const int block = __shfl_sync(0xffffffffu, src, j & 31);
-      if (j < my_n) {
-        if (lane == 0) issue(block, stage);
-        ++issued;
+      if (mine) {
+        const uint32_t bar = smem_u32(&sm.ring.full[w][stage]);
+        if (!is_v) {
+          // a bad page is flagged and block 0 loaded in its place
+          if (block < 0) flag_error(a.err, DEVERR_BAD_PAGE);
+          sm.bad[w][stage] = block < 0;
+          mbar_arrive_expect_tx(bar, kStageBytes);
+        }
+        tma_load_2d_hint(smem_u32(&sm.ring.slot[w][stage][0]) +
+                             (is_v ? kSliceBytes : 0),
+                         tm, head * kD, max(block, 0) * kPS, bar, policy);
       }
     }
-    if (failed) rows.clear();
+    if (!ok) {
+      if (lane == 0) flag_error(a.err, DEVERR_TIMEOUT);
+      // the copies in flight land before the CTA ends (bounded)
+      if (issuer && !is_v)
+        for (int k = max(0, i - kStages); k < i; ++k)
+          if (x0 + k * kW + w < x1)
+            mbar_wait(smem_u32(&sm.ring.full[w][k % kStages]),
+                      (k / kStages) & 1);
+    }
+  } else if (x0 < x1) {
+    // ======================= products ==========================================
+    uint32_t koff[4], voff[4];
+    slice_offsets(lane, koff, voff);
+    WarpRows<MB, kCausal> rows;
+    bool failed = false;
+    int stage = 0;
+    uint32_t parity = 0;
+    int x = x0 + warp;                  // the warp's next block
+    int seq = line.seq_of(x0);
+    int next_qs, next_T, next_ctx;
+    sequence_rows<kCausal>(a, seq, false, &next_qs, &next_T, &next_ctx);
+    for (int p0 = x0; p0 < x1;) {
+      const int base = sm.pre[seq];
+      const int end = min(x1, sm.pre[seq + 1]);
+      const int qs = next_qs, T = next_T, ctx = next_ctx;
+      int next_seq = seq;
+      if (end < x1) {   // the next sequence's rows, and its q into the cache
+        do ++next_seq; while (sm.pre[next_seq + 1] <= end);
+        sequence_rows<kCausal>(a, next_seq, false, &next_qs, &next_T,
+                               &next_ctx);
+        if (warp == 0 && lane < next_T << a.group_shift)
+          asm volatile("prefetch.global.L1 [%0];" ::"l"(
+              a.q + ((size_t)(next_qs + (lane >> a.group_shift)) *
+                         a.num_q_heads + (head << a.group_shift) +
+                     (lane & ((1 << a.group_shift) - 1))) * kD));
+      }
+      ChunkRows w;
+      w.q_row = qs;
+      w.tb = T;
+      w.first_limit = kCausal ? ctx - T : ctx - 1;
+      w.key_end = ctx;
+      rows.load(a, w, head, lane);
+      rows.clear();
+      for (; x < end && !failed; x += kW) {
+        if (!__all_sync(0xffffffffu,
+                        mbar_wait(smem_u32(&sm.ring.full[warp][stage]),
+                                  parity))) {
+          failed = true;
+          break;
+        }
+        if (rows.page(&sm.ring.slot[warp][stage][0], (x - base) * kPS,
+                      sm.bad[warp][stage] == 0, w, koff, voff, a.scale_log2,
+                      lane))
+          fence_proxy_async_smem();   // plain writes, before the next copy
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&sm.ring.empty[warp][stage]));
+        if (++stage == kStages) {
+          stage = 0;
+          parity ^= 1;
+        }
+      }
+      if (failed) rows.clear();
 
-    // ---- combine the warps; write, or leave a part ----------------------------------
-    rows.finish_sums();
-    const bool whole = p0 == base && end == sm.pre[seq + 1];
-    const int n_rows = T << a.group_shift;
-    float* part = a.ws_parts + ((size_t)blockIdx.x * 2 + (p0 == x0 ? 0 : 1)) *
-                                   kChunkPartFloats;
-    const int r16 = threadIdx.x >> 3, k8 = threadIdx.x & 7;
+      // ---- combine the warps; write, or leave a part --------------------------------
+      rows.finish_sums();
+      const bool whole = p0 == base && end == sm.pre[seq + 1];
+      const int n_rows = T << a.group_shift;
+      float* part = a.ws_parts + ((size_t)blockIdx.x * 2 + (p0 == x0 ? 0 : 1)) *
+                                     kChunkPartFloats;
+      const int r16 = threadIdx.x >> 3, k8 = threadIdx.x & 7;
 #pragma unroll
-    for (int b = 0; b < MB; ++b) {
-      if (16 * b >= n_rows) break;
-      __syncthreads();   // the last rows have been read
-      rows.put(sm.cb, b, warp, lane);
-      __syncthreads();
-      const int row = 16 * b + r16;
-      if (row >= n_rows) continue;
-      const Joined j = join_warps(sm.cb, r16, k8);
-      if (whole) {
-        j.write(out_row(a, qs, head, row), k8);
-      } else {
-        float4* dst = reinterpret_cast<float4*>(part + 2 * kChunkPartRows +
-                                                row * kD + 4 * k8);
-        __stcg(dst, j.x);
-        __stcg(dst + 8, j.y);
-        if (k8 == 0) {
-          __stcg(part + row, j.M);
-          __stcg(part + kChunkPartRows + row, j.L);
-        }
-      }
-    }
-    if (!whole) {
-      // groups whose boundary lies inside the sequence
-      const int z0 = base + kSnap, z1 = sm.pre[seq + 1] - kSnap;
-      const int g0 = (int)(((int64_t)z0 * NG + W - 1) / W);
-      const int g1 = (int)(((int64_t)(z1 + 1) * NG + W - 1) / W) - 1;
-      const int n_parts = g1 - g0 + 2;
-      __syncthreads();
-      int32_t* counter = a.ws_counters + (size_t)seq * Hkv + head;
-      if (threadIdx.x == 0) {
-        __threadfence();   // the CTA's part, ordered by the barrier
-        sm.last = atomicAdd(counter, 1) == n_parts - 1;
-        __threadfence();
-      }
-      __syncthreads();
-      if (sm.last) {
-        const bool first0 = cut(raw_cut(g0 - 1)) == base;
-        auto part_of = [&](int k) {   // part k is group g0 - 1 + k's
-          return a.ws_parts + ((size_t)((g0 - 1 + k) * Hkv + head) * 2 +
-                               (k == 0 && !first0 ? 1 : 0)) *
-                                  kChunkPartFloats;
-        };
-        for (int row = r16; row < n_rows; row += 16) {
-          Joined j;
-#pragma unroll 4
-          for (int k = 0; k < n_parts; ++k)
-            j.M = fmaxf(j.M, __ldcg(part_of(k) + row));
-#pragma unroll 4
-          for (int k = 0; k < n_parts; ++k) {
-            const float* p = part_of(k);
-            const float4* x = reinterpret_cast<const float4*>(
-                p + 2 * kChunkPartRows + row * kD + 4 * k8);
-            j.add(__ldcg(p + row), __ldcg(p + kChunkPartRows + row),
-                  __ldcg(x), __ldcg(x + 8));
-          }
+      for (int b = 0; b < MB; ++b) {
+        if (16 * b >= n_rows) break;
+        compute_barrier<kW>();   // the last rows have been read
+        rows.put(sm.cb, b, warp, lane);
+        compute_barrier<kW>();
+        const int row = 16 * b + r16;
+        if (r16 >= 16 || row >= n_rows) continue;
+        const Joined j = join_warps(sm.cb, r16, k8);
+        if (whole) {
           j.write(out_row(a, qs, head, row), k8);
+        } else {
+          float4* dst = reinterpret_cast<float4*>(part + 2 * kChunkPartRows +
+                                                  row * kD + 4 * k8);
+          __stcg(dst, j.x);
+          __stcg(dst + 8, j.y);
+          if (k8 == 0) {
+            __stcg(part + row, j.M);
+            __stcg(part + kChunkPartRows + row, j.L);
+          }
         }
-        if (threadIdx.x == 0) *counter = 0;
       }
+      if (!whole) {
+        // groups whose boundary lies inside the sequence
+        const int z0 = base + kSnap, z1 = sm.pre[seq + 1] - kSnap;
+        const int g0 = (int)(((int64_t)z0 * NG + W - 1) / W);
+        const int g1 = (int)(((int64_t)(z1 + 1) * NG + W - 1) / W) - 1;
+        const int n_parts = g1 - g0 + 2;
+        compute_barrier<kW>();
+        int32_t* counter = a.ws_counters + (size_t)seq * Hkv + head;
+        if (threadIdx.x == 0) {
+          __threadfence();   // the CTA's part, ordered by the barrier
+          sm.last = atomicAdd(counter, 1) == n_parts - 1;
+          __threadfence();
+        }
+        compute_barrier<kW>();
+        if (sm.last) {
+          const bool first0 = line.cut(g0 - 1) == base;
+          auto part_of = [&](int k) {   // part k is group g0 - 1 + k's
+            return a.ws_parts + ((size_t)((g0 - 1 + k) * Hkv + head) * 2 +
+                                 (k == 0 && !first0 ? 1 : 0)) *
+                                    kChunkPartFloats;
+          };
+          for (int row = r16; row < n_rows; row += kW * 4) {
+            Joined j;
+#pragma unroll 4
+            for (int k = 0; k < n_parts; ++k)
+              j.M = fmaxf(j.M, __ldcg(part_of(k) + row));
+#pragma unroll 4
+            for (int k = 0; k < n_parts; ++k) {
+              const float* q = part_of(k);
+              const float4* v = reinterpret_cast<const float4*>(
+                  q + 2 * kChunkPartRows + row * kD + 4 * k8);
+              j.add(__ldcg(q + row), __ldcg(q + kChunkPartRows + row),
+                    __ldcg(v), __ldcg(v + 8));
+            }
+            j.write(out_row(a, qs, head, row), k8);
+          }
+          if (threadIdx.x == 0) *counter = 0;
+        }
+      }
+      p0 = end;
+      seq = next_seq;
     }
-    p0 = end;
-    seq = next_seq;
-  }
-  if (failed) {
-    if (lane == 0) flag_error(a.err, DEVERR_TIMEOUT);
-    for (int k = i; k < issued; ++k)
-      mbar_wait(smem_u32(&sm.ring.full[warp][k % kStages]), (k / kStages) & 1);
+    if (failed && lane == 0) flag_error(a.err, DEVERR_TIMEOUT);
   }
   // the rows of the tile kernel are written when this kernel ends
   if (a.tile_ctas) wait_for_last_kernel();
 }
 
-static_assert(3 * (sizeof(BalancedSmem) + 1024 + 1024) <= 228 * 1024,
-              "three CTAs must fit in an SM's shared memory");
+static_assert(kChunkCtasPerSm * (sizeof(BalancedSmem<6>) + 1024 + 1024) <=
+                  228 * 1024,
+              "the CTAs of an SM must fit in its shared memory");
 
 template <int MB, bool kCausal>
 cudaError_t launch_mb(const ChunkArgs& a, const CUtensorMap& tk,
@@ -827,12 +915,13 @@ cudaError_t launch_mb(const ChunkArgs& a, const CUtensorMap& tk,
   // behind the tile kernel it fills the SMs that run out of tiles
   if (a.balanced_ctas)
     return launch_kernel<balanced_chunk_kernel<MB, kCausal>>(
-        dim3(a.balanced_ctas), kThreads, sizeof(BalancedSmem) + 1024,
+        dim3(a.balanced_ctas), (compute_warps(MB) + 1) * 32,
+        sizeof(BalancedSmem<compute_warps(MB)>) + 1024,
         a.tile_ctas > 0, stream, a, tk, tv);
   const int per = (16 * MB) >> a.group_shift;
   return launch_kernel<paged_chunk_kernel<MB, kCausal>>(
       dim3(a.num_kv_heads, a.num_seqs, (a.max_query_len + per - 1) / per),
-      kThreads, sizeof(ChunkRing) + 1024, false, stream, a, tk, tv);
+      kThreads, sizeof(ChunkRing<kWarps>) + 1024, false, stream, a, tk, tv);
 }
 
 }  // namespace

@@ -280,7 +280,7 @@ constexpr int kMinChunkBlocks = 16;     // 16-token blocks worth a CTA
 constexpr int kChunkPartRows = 32;      // rows x heads per KV head
 // m, l and the unscaled output of one part
 constexpr int kChunkPartFloats = kChunkPartRows * (2 + 64);
-constexpr int kChunkCtasPerSm = 3;
+constexpr int kChunkCtasPerSm = 2;
 // below so many visible keys P keeps 16 bits in P V, from there on 8
 constexpr int kChunkExactKeys = 512;
 // m, l and the unscaled output of two query tiles of 128 rows
