@@ -595,8 +595,14 @@ __global__ void __launch_bounds__(kThreads, 3)
 // 32 rows took it 670 of 2370 clocks.)
 constexpr int kSnap = 4;
 // A sub-core's 16,384 registers hold three warps of 32 rows or four of 16 rows
-// without spills: 6 or 7 warps a CTA, two CTAs an SM.
-__host__ __device__ constexpr int compute_warps(int mb) { return mb == 1 ? 6 : 5; }
+// without spills: two CTAs of 6 warps an SM, or three of 5 (more of them hide
+// one another's combines better).
+__host__ __device__ constexpr int compute_warps(int mb) {
+  return mb == 1 ? 4 : 5;
+}
+__host__ __device__ constexpr int ctas_per_sm(int mb) {
+  return mb == 1 ? kChunkCtasPerSm : 2;
+}
 
 template <int kW>
 struct BalancedSmem {
@@ -604,7 +610,7 @@ struct BalancedSmem {
   ChunkCombine<kW> cb;
   int32_t warp_total[kW + 1];
   int32_t items;
-  int32_t last;
+  int32_t last[2];
   uint32_t bad[kW][kStages];   // the slot's block was no page
   int32_t pre[kMaxChunkSeqs + 1];
 };
@@ -642,7 +648,8 @@ __device__ __forceinline__ void compute_barrier() {
 }
 
 template <int MB, bool kCausal>
-__global__ void __launch_bounds__((compute_warps(MB) + 1) * 32, kChunkCtasPerSm)
+__global__ void __launch_bounds__((compute_warps(MB) + 1) * 32,
+                                  ctas_per_sm(MB))
     balanced_chunk_kernel(const ChunkArgs a,
                           const __grid_constant__ CUtensorMap tm_k,
                           const __grid_constant__ CUtensorMap tm_v) {
@@ -786,10 +793,33 @@ __global__ void __launch_bounds__((compute_warps(MB) + 1) * 32, kChunkCtasPerSm)
     int seq = line.seq_of(x0);
     int next_qs, next_T, next_ctx;
     sequence_rows<kCausal>(a, seq, false, &next_qs, &next_T, &next_ctx);
+    ChunkRows w;
+    auto set_rows = [&]() {
+      w.q_row = next_qs;
+      w.tb = next_T;
+      w.first_limit = kCausal ? next_ctx - next_T : next_ctx - 1;
+      w.key_end = next_ctx;
+    };
+    set_rows();
+    rows.load(a, w, head, lane);
+    // Parts of the groups that a cut sequence is spread over: group g0 - 1 + k's
+    // is part k.
+    struct Parts {
+      int g0, n;
+    };
+    auto parts_of = [&](int s) {      // groups with a boundary inside it
+      const int z0 = sm.pre[s] + kSnap, z1 = sm.pre[s + 1] - kSnap;
+      const int g0 = (int)(((int64_t)z0 * NG + W - 1) / W);
+      const int g1 = (int)(((int64_t)(z1 + 1) * NG + W - 1) / W) - 1;
+      return Parts{g0, g1 - g0 + 2};
+    };
+    const int r16 = threadIdx.x >> 3, k8 = threadIdx.x & 7;
+    int cut_seq[2] = {-1, -1};        // the cut sequences of the range's ends
+    int counted[2] = {0, 0};          // thread 0: their counters before its own
     for (int p0 = x0; p0 < x1;) {
       const int base = sm.pre[seq];
       const int end = min(x1, sm.pre[seq + 1]);
-      const int qs = next_qs, T = next_T, ctx = next_ctx;
+      const int q_row = w.q_row, n_rows = w.tb << a.group_shift;
       int next_seq = seq;
       if (end < x1) {   // the next sequence's rows, and its q into the cache
         do ++next_seq; while (sm.pre[next_seq + 1] <= end);
@@ -801,12 +831,6 @@ __global__ void __launch_bounds__((compute_warps(MB) + 1) * 32, kChunkCtasPerSm)
                          a.num_q_heads + (head << a.group_shift) +
                      (lane & ((1 << a.group_shift) - 1))) * kD));
       }
-      ChunkRows w;
-      w.q_row = qs;
-      w.tb = T;
-      w.first_limit = kCausal ? ctx - T : ctx - 1;
-      w.key_end = ctx;
-      rows.load(a, w, head, lane);
       rows.clear();
       for (; x < end && !failed; x += kW) {
         if (!__all_sync(0xffffffffu,
@@ -827,14 +851,17 @@ __global__ void __launch_bounds__((compute_warps(MB) + 1) * 32, kChunkCtasPerSm)
         }
       }
       if (failed) rows.clear();
+      if (end < x1) {   // the next q, in flight during the combine
+        set_rows();
+        rows.load(a, w, head, lane);
+      }
 
       // ---- combine the warps; write, or leave a part --------------------------------
       rows.finish_sums();
       const bool whole = p0 == base && end == sm.pre[seq + 1];
-      const int n_rows = T << a.group_shift;
-      float* part = a.ws_parts + ((size_t)blockIdx.x * 2 + (p0 == x0 ? 0 : 1)) *
-                                     kChunkPartFloats;
-      const int r16 = threadIdx.x >> 3, k8 = threadIdx.x & 7;
+      const int slot = p0 == x0 ? 0 : 1;
+      float* part =
+          a.ws_parts + ((size_t)blockIdx.x * 2 + slot) * kChunkPartFloats;
 #pragma unroll
       for (int b = 0; b < MB; ++b) {
         if (16 * b >= n_rows) break;
@@ -845,7 +872,7 @@ __global__ void __launch_bounds__((compute_warps(MB) + 1) * 32, kChunkCtasPerSm)
         if (r16 >= 16 || row >= n_rows) continue;
         const Joined j = join_warps(sm.cb, r16, k8);
         if (whole) {
-          j.write(out_row(a, qs, head, row), k8);
+          j.write(out_row(a, q_row, head, row), k8);
         } else {
           float4* dst = reinterpret_cast<float4*>(part + 2 * kChunkPartRows +
                                                   row * kD + 4 * k8);
@@ -858,46 +885,60 @@ __global__ void __launch_bounds__((compute_warps(MB) + 1) * 32, kChunkCtasPerSm)
         }
       }
       if (!whole) {
-        // groups whose boundary lies inside the sequence
-        const int z0 = base + kSnap, z1 = sm.pre[seq + 1] - kSnap;
-        const int g0 = (int)(((int64_t)z0 * NG + W - 1) / W);
-        const int g1 = (int)(((int64_t)(z1 + 1) * NG + W - 1) / W) - 1;
-        const int n_parts = g1 - g0 + 2;
+        // count the part; what the count says is looked at when the range is done
+        cut_seq[slot] = seq;
         compute_barrier<kW>();
-        int32_t* counter = a.ws_counters + (size_t)seq * Hkv + head;
         if (threadIdx.x == 0) {
           __threadfence();   // the CTA's part, ordered by the barrier
-          sm.last = atomicAdd(counter, 1) == n_parts - 1;
-          __threadfence();
-        }
-        compute_barrier<kW>();
-        if (sm.last) {
-          const bool first0 = line.cut(g0 - 1) == base;
-          auto part_of = [&](int k) {   // part k is group g0 - 1 + k's
-            return a.ws_parts + ((size_t)((g0 - 1 + k) * Hkv + head) * 2 +
-                                 (k == 0 && !first0 ? 1 : 0)) *
-                                    kChunkPartFloats;
-          };
-          for (int row = r16; row < n_rows; row += kW * 4) {
-            Joined j;
-#pragma unroll 4
-            for (int k = 0; k < n_parts; ++k)
-              j.M = fmaxf(j.M, __ldcg(part_of(k) + row));
-#pragma unroll 4
-            for (int k = 0; k < n_parts; ++k) {
-              const float* q = part_of(k);
-              const float4* v = reinterpret_cast<const float4*>(
-                  q + 2 * kChunkPartRows + row * kD + 4 * k8);
-              j.add(__ldcg(q + row), __ldcg(q + kChunkPartRows + row),
-                    __ldcg(v), __ldcg(v + 8));
-            }
-            j.write(out_row(a, qs, head, row), k8);
-          }
-          if (threadIdx.x == 0) *counter = 0;
+          counted[slot] =
+              atomicAdd(a.ws_counters + (size_t)seq * Hkv + head, 1);
         }
       }
       p0 = end;
       seq = next_seq;
+    }
+
+    // ---- cut sequences whose last part was this CTA's: join the parts ----------------
+    if (cut_seq[0] >= 0 || cut_seq[1] >= 0) {
+      if (threadIdx.x == 0) {
+#pragma unroll
+        for (int e = 0; e < 2; ++e)
+          sm.last[e] =
+              cut_seq[e] >= 0 && counted[e] == parts_of(cut_seq[e]).n - 1;
+        __threadfence();
+      }
+      compute_barrier<kW>();
+#pragma unroll 1
+      for (int e = 0; e < 2; ++e) {
+        if (!sm.last[e]) continue;
+        const int s = cut_seq[e];
+        const Parts parts = parts_of(s);
+        const bool first0 = line.cut(parts.g0 - 1) == sm.pre[s];
+        auto part_of = [&](int k) {
+          return a.ws_parts +
+                 ((size_t)((parts.g0 - 1 + k) * Hkv + head) * 2 +
+                  (k == 0 && !first0 ? 1 : 0)) *
+                     kChunkPartFloats;
+        };
+        int qs, T, ctx;
+        sequence_rows<kCausal>(a, s, false, &qs, &T, &ctx);
+        for (int row = r16; row < T << a.group_shift; row += kW * 4) {
+          Joined j;
+#pragma unroll 4
+          for (int k = 0; k < parts.n; ++k)
+            j.M = fmaxf(j.M, __ldcg(part_of(k) + row));
+#pragma unroll 4
+          for (int k = 0; k < parts.n; ++k) {
+            const float* q = part_of(k);
+            const float4* v = reinterpret_cast<const float4*>(
+                q + 2 * kChunkPartRows + row * kD + 4 * k8);
+            j.add(__ldcg(q + row), __ldcg(q + kChunkPartRows + row),
+                  __ldcg(v), __ldcg(v + 8));
+          }
+          j.write(out_row(a, qs, head, row), k8);
+        }
+        if (threadIdx.x == 0) a.ws_counters[(size_t)s * Hkv + head] = 0;
+      }
     }
     if (failed && lane == 0) flag_error(a.err, DEVERR_TIMEOUT);
   }
@@ -905,8 +946,13 @@ __global__ void __launch_bounds__((compute_warps(MB) + 1) * 32, kChunkCtasPerSm)
   if (a.tile_ctas) wait_for_last_kernel();
 }
 
-static_assert(kChunkCtasPerSm * (sizeof(BalancedSmem<6>) + 1024 + 1024) <=
-                  228 * 1024,
+template <int MB>
+constexpr bool fits() {
+  return ctas_per_sm(MB) *
+             (sizeof(BalancedSmem<compute_warps(MB)>) + 1024 + 1024) <=
+         228 * 1024;
+}
+static_assert(fits<1>() && fits<2>(),
               "the CTAs of an SM must fit in its shared memory");
 
 template <int MB, bool kCausal>
@@ -915,7 +961,8 @@ cudaError_t launch_mb(const ChunkArgs& a, const CUtensorMap& tk,
   // behind the tile kernel it fills the SMs that run out of tiles
   if (a.balanced_ctas)
     return launch_kernel<balanced_chunk_kernel<MB, kCausal>>(
-        dim3(a.balanced_ctas), (compute_warps(MB) + 1) * 32,
+        dim3(a.balanced_ctas / kChunkCtasPerSm * ctas_per_sm(MB)),
+        (compute_warps(MB) + 1) * 32,
         sizeof(BalancedSmem<compute_warps(MB)>) + 1024,
         a.tile_ctas > 0, stream, a, tk, tv);
   const int per = (16 * MB) >> a.group_shift;

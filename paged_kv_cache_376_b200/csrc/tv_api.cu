@@ -909,7 +909,7 @@ static tv_status chunk_common(void* out, const void* q, int64_t num_query_rows,
   // the balanced grid holds every sequence's prefix sum in shared memory and
   // counts blocks in 32 bits
   if (workspace && num_seqs <= tv::kMaxChunkSeqs &&
-      num_kv_heads <= chunk_ctas() &&
+      num_kv_heads <= device_sms() &&
       ((int64_t)num_seqs * max_blocks_per_seq << a.page_shift) <= INT32_MAX) {
     char* base = static_cast<char*>(workspace);
     a.balanced_ctas = chunk_ctas();

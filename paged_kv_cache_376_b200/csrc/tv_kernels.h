@@ -264,7 +264,7 @@ struct ChunkArgs {
   int group_shift;               // query heads per KV head = 1 << group_shift
   // With a workspace: CTAs of the balanced grid (0: one CTA per KV head, row
   // block and sequence), which serves the sequences of up to stream_rows rows.
-  int balanced_ctas;
+  int balanced_ctas;             // kChunkCtasPerSm per SM
   int stream_rows;
   int32_t* ws_counters;          // [B][Hkv], zero between calls
   float* ws_parts;               // [balanced_ctas][2][kChunkPartFloats]
@@ -280,7 +280,7 @@ constexpr int kMinChunkBlocks = 16;     // 16-token blocks worth a CTA
 constexpr int kChunkPartRows = 32;      // rows x heads per KV head
 // m, l and the unscaled output of one part
 constexpr int kChunkPartFloats = kChunkPartRows * (2 + 64);
-constexpr int kChunkCtasPerSm = 2;
+constexpr int kChunkCtasPerSm = 3;     // at most
 // below so many visible keys P keeps 16 bits in P V, from there on 8
 constexpr int kChunkExactKeys = 512;
 // m, l and the unscaled output of two query tiles of 128 rows
