@@ -91,6 +91,7 @@ SIGNATURES = {
 }
 
 _lib = None
+_fast = None    # the C++ side of the ordinary calls (csrc/fastcall.cpp)
 
 
 class TVError(RuntimeError):
@@ -111,6 +112,9 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
         fn = getattr(lib, name)
         fn.restype = res
         fn.argtypes = args
+    global _fast
+    from . import _fastcall
+    _fast = _fastcall
     _lib = lib
     return lib
 
@@ -148,9 +152,9 @@ def _stream(stream):
     return ctypes.c_void_p(stream.cuda_stream)
 
 
-# The calls below check about ten tensors each; at a few microseconds of GPU
-# time that is what a small call costs, so the checks are one pass over cheap
-# attributes, and the device and stream come from torch's plain accessors.
+# The serving operators' ordinary calls go through csrc/fastcall.cpp; the checks
+# here are for the forms it leaves (a stream of its own, another device) and
+# for saying what is wrong.
 def _one_device(tensors, stream):
     """Device index and stream pointer of a call on ``tensors`` (None entries
     skipped): all of them on one device, the stream on it too."""
@@ -273,6 +277,10 @@ def tv_kv_append_mrope(q_out, q, k_new, v_new, slot_mapping, positions,
     table as tv_kv_append_rope), q into q_out [T][Hq][D], K and V into their
     slots.  q, k_new, v_new [T][H][D] may have strided token rows; positions
     is [axes][T], pair_axis [D/2] int32.  q and q_out None: K and V only."""
+    if stream is None and _fast and _fast.mrope(
+            q_out, q, k_new, v_new, slot_mapping, positions, pair_axis,
+            k_pool, v_pool, cos_sin, err):
+        return
     if (q is None) != (q_out is None):
         raise ValueError("q and q_out go together")
     ks, vs = _token_rows(k_new, "k_new"), _token_rows(v_new, "v_new")
@@ -533,6 +541,10 @@ def tv_paged_chunk(out, q, query_start_loc, k_pool, v_pool, block_tables,
     """out[rows][Hq][D] (bf16) = causal attention of a chunk of new rows per
     sequence (one row to long chunks in one call) over the paged cache; with
     a ``workspace`` (chunk_workspace) long contexts are split over keys."""
+    if stream is None and _fast and _fast.chunk(
+            True, out, q, query_start_loc, k_pool, v_pool, block_tables,
+            context_lens, scale, max_query_len, workspace, err):
+        return
     _chunk("tv_paged_chunk", out, q, query_start_loc, k_pool, v_pool,
            block_tables, context_lens, "context_lens", scale, max_query_len,
            workspace, err, stream)
@@ -544,6 +556,10 @@ def tv_paged_cross_attention(out, q, query_start_loc, k_pool, v_pool,
                              stream=None):
     """out[rows][Hq][D] (bf16) = attention of every query row of sequence s to
     all encoder_lens[s] cached encoder states (no mask)."""
+    if stream is None and _fast and _fast.chunk(
+            False, out, q, query_start_loc, k_pool, v_pool, block_tables,
+            encoder_lens, scale, max_query_len, workspace, err):
+        return
     _chunk("tv_paged_cross_attention", out, q, query_start_loc, k_pool,
            v_pool, block_tables, encoder_lens, "encoder_lens", scale,
            max_query_len, workspace, err, stream)
@@ -733,6 +749,9 @@ def tv_pool_truncate(state, block_tables, context_lens, new_lens, err=None,
                      stream=None):
     """Every sequence keeps its first new_lens[s] tokens; pages behind them
     that nobody else holds go back to the pool."""
+    if stream is None and _fast and _fast.truncate(
+            state, block_tables, context_lens, new_lens, err):
+        return
     num_pages = _pool_pages(state)
     mb, b = _pool_tables(block_tables, context_lens)
     _all_cuda(torch.int32, new_lens=new_lens, err=err)
@@ -759,6 +778,10 @@ def tv_pool_compact(state, block_tables, context_lens, moves, num_moves,
     """Pages in use move to the front of the pool; moves[0][:n] -> moves[1][:n]
     with n = num_moves (see pool_moves) lists them for tv_page_copy on further
     layers' pools.  page_size is the pools' when they are given."""
+    if stream is None and page_size is None and _fast and _fast.compact(
+            state, block_tables, context_lens, moves, num_moves, k_pool,
+            v_pool, err):
+        return
     num_pages = _pool_pages(state)
     mb, b = _pool_tables(block_tables, context_lens)
     _all_cuda(torch.int32, moves=moves, num_moves=num_moves, err=err)
@@ -788,6 +811,9 @@ def tv_page_copy(k_pool, v_pool, src_pages, dst_pages, num_pairs=None,
                  err=None, stream=None):
     """Copy whole pages src_pages[i] -> dst_pages[i] of both pools, all of
     them or the first num_pairs (a device int32)."""
+    if stream is None and _fast and _fast.page_copy(
+            k_pool, v_pool, src_pages, dst_pages, num_pairs, err):
+        return
     _all_cuda(torch.bfloat16, k_pool=k_pool, v_pool=v_pool)
     _all_cuda(torch.int32, src_pages=src_pages, dst_pages=dst_pages,
               num_pairs=num_pairs, err=err)

@@ -19,6 +19,8 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB_PATH = os.path.join(PKG, "libtv.so")
+FAST_PATH = os.path.join(PKG, "_fastcall.so")
+FAST_SOURCE = os.path.join(CSRC, "fastcall.cpp")
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 
 
@@ -46,7 +48,42 @@ def up_to_date() -> bool:
     return all(os.path.getmtime(p) <= t for p in _inputs())
 
 
+def _build_fastcall(verbose: bool = False) -> None:
+    """_fastcall.so: the C++ side of _lib's ordinary calls (torch's headers,
+    libtv's C calls)."""
+    import sysconfig
+
+    import torch
+    root = os.path.join(os.path.dirname(torch.__file__))
+    inc = os.path.join(root, "include")
+    tmp = FAST_PATH + f".tmp{os.getpid()}"
+    cuda = os.path.dirname(os.path.dirname(os.path.realpath(_nvcc())))
+    cmd = [shutil.which("g++") or "g++", "-O2", "-std=c++17", "-fPIC",
+           "-shared",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+           "-I", INCLUDE, "-isystem", inc, "-isystem",
+           os.path.join(inc, "torch", "csrc", "api", "include"), "-isystem",
+           os.path.join(cuda, "include"), "-isystem",
+           sysconfig.get_paths()["include"], FAST_SOURCE, "-o", tmp,
+           "-L", os.path.join(root, "lib"), "-ltorch_python", "-ltorch",
+           "-ltorch_cpu", "-lc10", "-lc10_cuda", "-L", PKG, "-l:libtv.so",
+           "-Wl,-rpath,$ORIGIN"]
+    if verbose:
+        print(" ".join(cmd), flush=True)
+    subprocess.run(cmd, check=True)
+    os.replace(tmp, FAST_PATH)
+
+
 def build(force: bool = False, verbose: bool = False) -> str:
+    _build_lib(force, verbose)
+    need = [FAST_SOURCE, os.path.join(INCLUDE, "tv.h")]
+    if force or not os.path.exists(FAST_PATH) or any(
+            os.path.getmtime(p) > os.path.getmtime(FAST_PATH) for p in need):
+        _build_fastcall(verbose)
+    return LIB_PATH
+
+
+def _build_lib(force: bool = False, verbose: bool = False) -> str:
     if not force and up_to_date():
         return LIB_PATH
     tmp = LIB_PATH + f".tmp{os.getpid()}"
