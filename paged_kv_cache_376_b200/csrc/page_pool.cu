@@ -643,26 +643,38 @@ __device__ __forceinline__ void copy_pages(uint4* k_pool, uint4* v_pool,
                                            int64_t cta, int64_t ctas,
                                            uint32_t* err) {
   const int per = (page_vecs + kUnitVecs - 1) / kUnitVecs;   // units of a page
-  const int64_t units = n * 2 * per;
+  // unit = (pair, r), r < per: K, else V; a step of `ctas` units by addition
+  // (a 64-bit division per unit costs as much as its copy)
+  const int both = 2 * per;
+  const int64_t pair_step = ctas / both;
+  const int r_step = (int)(ctas % both);
+  int64_t pair = cta / both;
+  int r = (int)(cta % both);
   int a = 0, b = 0;
-  if (cta < units) {
-    a = __ldcg(src + cta / (2 * per));
-    b = __ldcg(dst + cta / (2 * per));
+  if (pair < n) {
+    a = __ldcg(src + pair);
+    b = __ldcg(dst + pair);
   }
-  for (int64_t i = cta; i < units; i += ctas) {
-    const int r = (int)(i % (2 * per));
-    const int from_page = a, to_page = b;
-    if (i + ctas < units) {
-      a = __ldcg(src + (i + ctas) / (2 * per));
-      b = __ldcg(dst + (i + ctas) / (2 * per));
+  while (pair < n) {
+    const int from_page = a, to_page = b, unit = r;
+    pair += pair_step;
+    r += r_step;
+    if (r >= both) {
+      r -= both;
+      ++pair;
+    }
+    if (pair < n) {
+      a = __ldcg(src + pair);
+      b = __ldcg(dst + pair);
     }
     if (from_page < 0 || from_page >= num_pages || to_page < 0 ||
         to_page >= num_pages) {
-      if (threadIdx.x == 0 && r == 0) flag_error(err, DEVERR_BAD_PAGE);
+      if (threadIdx.x == 0 && unit == 0) flag_error(err, DEVERR_BAD_PAGE);
       continue;
     }
-    uint4* pool = r < per ? k_pool : v_pool;
-    const int v0 = (r < per ? r : r - per) * kUnitVecs + threadIdx.x;
+    uint4* pool = unit < per ? k_pool : v_pool;
+    const int v0 =
+        (unit < per ? unit : unit - per) * kUnitVecs + threadIdx.x;
     const uint4* from = pool + (size_t)from_page * page_vecs;
     uint4* to = pool + (size_t)to_page * page_vecs;
     uint4 x[2];
