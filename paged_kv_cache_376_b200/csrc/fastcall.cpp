@@ -75,11 +75,28 @@ PyObject* done(bool made) {
   Py_RETURN_FALSE;
 }
 
+// A tensor that has no strides, or no memory, throws when asked for them; that
+// ends here, not in the interpreter.
+using Function = PyObject* (*)(PyObject* const*, Py_ssize_t);
+template <Function kFunction>
+PyObject* guarded(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  try {
+    return kFunction(a, n);
+  } catch (...) {
+    return done(false);
+  }
+}
+template <Function kFunction>
+PyMethodDef method(const char* name) {
+  return {name, (PyCFunction)(void (*)())guarded<kFunction>, METH_FASTCALL,
+          nullptr};
+}
+
 bool fits_int(int64_t v) { return v >= 0 && v <= INT32_MAX; }
 
 // chunk(causal, out, q, query_start_loc, k_pool, v_pool, block_tables, lens,
 //       scale, max_query_len, workspace, err)
-PyObject* chunk(PyObject*, PyObject* const* a, Py_ssize_t n) {
+PyObject* chunk(PyObject* const* a, Py_ssize_t n) {
   if (n != 12) return done(false);
   Call c;
   const int causal = PyObject_IsTrue(a[0]);
@@ -119,7 +136,7 @@ PyObject* chunk(PyObject*, PyObject* const* a, Py_ssize_t n) {
 
 // mrope(q_out, q, k_new, v_new, slot_mapping, positions, pair_axis, k_pool,
 //       v_pool, cos_sin, err), q and q_out not None
-PyObject* mrope(PyObject*, PyObject* const* a, Py_ssize_t n) {
+PyObject* mrope(PyObject* const* a, Py_ssize_t n) {
   if (n != 11) return done(false);
   Call c;
   const at::Tensor* out = c.bf16(a[0]);
@@ -168,7 +185,7 @@ int64_t pool_pages(const at::Tensor* state) {
 }
 
 // truncate(state, block_tables, context_lens, new_lens, err)
-PyObject* truncate(PyObject*, PyObject* const* a, Py_ssize_t n) {
+PyObject* truncate(PyObject* const* a, Py_ssize_t n) {
   if (n != 5) return done(false);
   Call c;
   const at::Tensor* state = c.ints(a[0]);
@@ -190,7 +207,7 @@ PyObject* truncate(PyObject*, PyObject* const* a, Py_ssize_t n) {
 
 // compact(state, block_tables, context_lens, moves, num_moves, k_pool, v_pool,
 //         err), pools not None
-PyObject* compact(PyObject*, PyObject* const* a, Py_ssize_t n) {
+PyObject* compact(PyObject* const* a, Py_ssize_t n) {
   if (n != 8) return done(false);
   Call c;
   const at::Tensor* state = c.ints(a[0]);
@@ -220,7 +237,7 @@ PyObject* compact(PyObject*, PyObject* const* a, Py_ssize_t n) {
 }
 
 // page_copy(k_pool, v_pool, src_pages, dst_pages, num_pairs, err)
-PyObject* page_copy(PyObject*, PyObject* const* a, Py_ssize_t n) {
+PyObject* page_copy(PyObject* const* a, Py_ssize_t n) {
   if (n != 6) return done(false);
   Call c;
   const at::Tensor* k = c.bf16(a[0]);
@@ -242,12 +259,9 @@ PyObject* page_copy(PyObject*, PyObject* const* a, Py_ssize_t n) {
 }
 
 PyMethodDef kMethods[] = {
-    {"chunk", (PyCFunction)(void (*)())chunk, METH_FASTCALL, nullptr},
-    {"mrope", (PyCFunction)(void (*)())mrope, METH_FASTCALL, nullptr},
-    {"truncate", (PyCFunction)(void (*)())truncate, METH_FASTCALL, nullptr},
-    {"compact", (PyCFunction)(void (*)())compact, METH_FASTCALL, nullptr},
-    {"page_copy", (PyCFunction)(void (*)())page_copy, METH_FASTCALL, nullptr},
-    {nullptr, nullptr, 0, nullptr}};
+    method<chunk>("chunk"),         method<mrope>("mrope"),
+    method<truncate>("truncate"),   method<compact>("compact"),
+    method<page_copy>("page_copy"), {nullptr, nullptr, 0, nullptr}};
 
 PyModuleDef kModule = {PyModuleDef_HEAD_INIT, "_fastcall",
                        "The serving operators' ordinary calls.", -1, kMethods,
