@@ -526,8 +526,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 // the i-th free page below U; both lists are ascending and equally long.  Then
 // the pages in use are exactly 0 .. U - 1 and the free stack is rebuilt as init
 // leaves it.  This kernel (one CTA, latency-bound) plans: counts as bit words,
-// eight words a warp in flight, their scan, the move lists, the counts and the
-// stack.
+// sixteen words a warp in flight, their scan, the move lists and the stack.
 constexpr int kHeldWords = 4096;   // bit words kept in shared memory
 
 __global__ void __launch_bounds__(kThreads, 1)
@@ -551,7 +550,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       on_chip ? sh_held : reinterpret_cast<uint32_t*>(p.cnt_app);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   int mine = 0;
-  constexpr int kU = 8;
+  constexpr int kU = 16;
   for (int w0 = warp * kU; w0 < words; w0 += kU * (kThreads / 32)) {
     int r[kU];
 #pragma unroll
@@ -586,12 +585,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         return ~b & low(w);
       },
       [&](int i, int page) { move_dst[i] = page; });
-  __syncthreads();
-  for (int i = threadIdx.x; i < ns; i += kThreads) {
-    const int a = move_src[i], b = move_dst[i];
-    p.ref[b] = p.ref[a];
-    p.ref[a] = 0;
-  }
   for (int i = threadIdx.x; i < n - used; i += kThreads)
     p.stack[i] = n - 1 - i;
   if (threadIdx.x == 0) {
@@ -600,15 +593,21 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
-// Block-table entries follow their pages: a binary search in the ascending
-// list of moved pages (entries below its first page did not move).
-__device__ __forceinline__ void move_entries(int32_t* bt, int mb,
+// Counts and block-table entries follow their pages, the entries by a binary
+// search in the ascending list of moved pages (those below its first page did
+// not move).
+__device__ __forceinline__ void move_entries(int32_t* ref, int32_t* bt, int mb,
                                              const int32_t* ctx, int num_seqs,
                                              int kPS, const int32_t* move_src,
                                              const int32_t* move_dst, int n,
                                              int cta, int ctas,
                                              uint32_t* err) {
   const int first = n > 0 ? __ldcg(move_src) : 0;
+  for (int i = cta * blockDim.x + threadIdx.x; i < n; i += ctas * blockDim.x) {
+    const int a = __ldcg(move_src + i), b = __ldcg(move_dst + i);
+    ref[b] = ref[a];
+    ref[a] = 0;
+  }
   const int64_t total = (int64_t)num_seqs * mb;
   for (int64_t i = cta * (int64_t)blockDim.x + threadIdx.x; i < total;
        i += (int64_t)ctas * blockDim.x) {
@@ -692,6 +691,7 @@ __global__ void __launch_bounds__(256)
                      int page_vecs, const int32_t* src, const int32_t* dst,
                      int64_t max_pairs, const int32_t* num_pairs,
                      uint32_t* err) {
+  wait_for_last_kernel();   // the lists, and what wrote the pages
   int64_t n = max_pairs;
   if (num_pairs) {
     n = *num_pairs;
@@ -702,18 +702,19 @@ __global__ void __launch_bounds__(256)
 }
 
 // What the plan leaves to do, in one launch that starts beside the plan: the
-// first table_ctas CTAs move the entries, the others copy pages.
+// first table_ctas CTAs move counts and entries, the others copy pages.
 __global__ void __launch_bounds__(256)
-    pool_compact_move_kernel(int32_t* bt, int mb, const int32_t* ctx,
+    pool_compact_move_kernel(int32_t* ref, int32_t* bt, int mb, const int32_t* ctx,
                              int num_seqs, int kPS, int table_ctas,
                              const int32_t* move_src, const int32_t* move_dst,
                              const int32_t* num_moves, uint4* k_pool,
                              uint4* v_pool, int num_pages, int page_vecs,
                              uint32_t* err) {
+  let_next_kernel_start();
   wait_for_last_kernel();
   const int n = __ldcg(num_moves);
   if ((int)blockIdx.x < table_ctas)
-    move_entries(bt, mb, ctx, num_seqs, kPS, move_src, move_dst, n,
+    move_entries(ref, bt, mb, ctx, num_seqs, kPS, move_src, move_dst, n,
                  blockIdx.x, table_ctas, err);
   else
     copy_pages(k_pool, v_pool, num_pages, page_vecs, move_src, move_dst, n,
@@ -750,15 +751,14 @@ cudaError_t launch_pool_compact(int32_t* state, int num_pages, int page_size,
       view(state, num_pages), page_size, move_src, move_dst, num_moves, err);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
-  const int64_t want = ((int64_t)num_seqs * mb + 255) / 256;
+  const int64_t want = ((int64_t)num_seqs * mb + 255) / 256 + 1;
   const int64_t cap = (int64_t)device_sm_count() * 2;
   const int table_ctas = (int)(want < cap ? want : cap);
   const int page_vecs = page_size * row_bytes / 16;
   const int ctas =
       table_ctas + (k_pool ? copy_ctas(num_pages / 2, page_vecs) : 0);
-  if (ctas == 0) return cudaSuccess;
   return launch_kernel<pool_compact_move_kernel>(
-      dim3(ctas), 256, 0, true, stream, bt, mb, ctx, num_seqs, page_size,
+      dim3(ctas), 256, 0, true, stream, view(state, num_pages).ref, bt, mb, ctx, num_seqs, page_size,
       table_ctas, (const int32_t*)move_src, (const int32_t*)move_dst,
       (const int32_t*)num_moves, static_cast<uint4*>(k_pool),
       static_cast<uint4*>(v_pool), num_pages, page_vecs, err);
@@ -771,10 +771,11 @@ cudaError_t launch_page_copy(void* k_pool, void* v_pool, int num_pages,
                              cudaStream_t stream) {
   if (max_pairs == 0) return cudaSuccess;
   const int page_vecs = page_bytes / 16;
-  page_copy_kernel<<<copy_ctas(max_pairs, page_vecs), 256, 0, stream>>>(
+  // (starts beside a compaction that it follows)
+  return launch_kernel<page_copy_kernel>(
+      dim3(copy_ctas(max_pairs, page_vecs)), 256, 0, true, stream,
       static_cast<uint4*>(k_pool), static_cast<uint4*>(v_pool), num_pages,
       page_vecs, src, dst, max_pairs, num_pairs, err);
-  return cudaGetLastError();
 }
 
 cudaError_t launch_pool_init(int32_t* state, int num_pages, int page_size,
