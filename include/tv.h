@@ -418,7 +418,13 @@ tv_status tv_prefill_workspace_size(int num_seqs, int max_query_len,
  * A sequence with T_s > C, T_s > max_query_len or rows outside q is flagged
  * TV_DEVERR_BAD_QUERY and skipped.  scale must be positive
  * (TV_ERR_INVALID_ARG otherwise, as tv_paged_prefill); max_query_len times the
- * group size is at most 2^20 - 16.  A key of a bad page is left out; a row
+ * group size is at most 2^20 - 16.  Scores, weights, their sum and the output's
+ * sum are fp32; the weights enter the product with V in bf16, with 16 bits for
+ * rows of a block whose first row sees fewer than 512 keys.  With a workspace,
+ * up to 1024 sequences (and max_blocks_per_seq * page_size * num_seqs / 16 up
+ * to 2^31 - 1) are split over keys, and sequences of more than 32 rows x heads
+ * per KV head run on the tcgen05 tensor cores.  A key of a bad page is left
+ * out; a row
  * that sees no key comes out zero.  What a key that a row does not see holds,
  * NaN and infinities too, does not reach that row; an infinity or NaN in V
  * that it sees makes that element of its output non-finite.

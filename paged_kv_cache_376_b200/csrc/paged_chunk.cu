@@ -7,21 +7,26 @@
 // The softmax is online: a running maximum m and sum l per row, O rescaled
 // when m moves.
 //
-// What bounds it: a sequence's K and V are read once for all of its rows, so
-// up to about 64 rows x heads per KV head the work is the HBM stream.
+// What bounds it: a sequence's K and V are read once for up to 32 rows x heads
+// per KV head, and that stream from HBM is the floor.  Up to 16 rows it is also
+// the bound (8 x 131072 tokens, 16 rows: 322 us, 6.7 TB/s); with 32 a warp's
+// step of 1060 clocks a page, a chain of products, exponentials and products
+// with 2.5 warps per scheduler to hide it, takes longer than the page's bytes
+// (64 x 2048 tokens: 64 us, where the stream takes 41).
 //
-// Design.  One CTA of 4 warps per (KV head, block of rows, sequence); every
-// warp streams its own pages w, w + 4, ... through a private ring of TMA
-// boxes (16 tokens x 128 B of K and of V, 128-byte swizzle), so no warp waits
-// for another before the final combine.  A row of the product is one (query
-// row, head of the KV head's group) pair, row r = query row r / G, head
-// r % G, 16 * MB rows per block.  Per page a warp forms S = Q K^T and
-// O += P V with m16n8k16 bf16 products and fp32 accumulators: with at least
-// 16 rows, rows in the M dimension put P's accumulator fragment where the
-// next product wants its A operand, so P needs no shuffles (the decode
-// kernels, with at most 8 rows, put tokens in M instead).
+// Design.  Every warp works on pages of its own, which reach it through a
+// private ring of TMA boxes (16 tokens x 128 B of K and of V, 128-byte
+// swizzle), so no warp waits for another before a sequence's rows are combined.
+// A row of the product is one (query row, head of the KV head's group) pair,
+// row r = query row r / G, head r % G, 16 * MB rows per block.  Per page a
+// warp forms S = Q K^T and O += P V with m16n8k16 bf16 products and fp32
+// accumulators: with at least 16 rows, rows in the M dimension put P's
+// accumulator fragment where the next product wants its A operand, so P needs
+// no shuffles (the decode kernels, with at most 8 rows, put tokens in M
+// instead).  Two kernels share this step: one CTA per (KV head, block of rows,
+// sequence), for calls without a workspace, and a balanced grid.
 //
-// P enters the second product in bf16.  A weight's rounding (2^-9 of it)
+// P enters the second product in bf16.  A weight's rounding (up to 2^-8)
 // averages out over the keys of a row, except where there are few: blocks
 // whose first row sees fewer than kChunkExactKeys keys add P's remainder,
 // P - bf16(P), with a second product, as the decode and the prefill always do.
@@ -591,8 +596,10 @@ __global__ void __launch_bounds__(kThreads, 3)
 // W warps compute, block x0 + w + W i the i-th of warp w; one more looks the
 // blocks up and issues the loads into their rings.  The rings run across
 // sequence ends: the loads of the next sequence are in flight while the last
-// one's warps are combined.  (With each warp issuing its own loads a block of
-// 32 rows took it 670 of 2370 clocks.)
+// one's warps are combined.  (With each warp issuing its own loads, that took
+// it 670 of the 2370 clocks of a page of 32 rows.)  64 x 2048 tokens, 32 rows:
+// one CTA per sequence and KV head 74 us (512 CTAs on 444 places), this 64;
+// 8 x 131072: 1172 and 322.
 constexpr int kSnap = 4;
 // A sub-core's 16,384 registers hold three warps of 32 rows or four of 16 rows
 // without spills: two CTAs of 6 warps an SM, or three of 5 (more of them hide

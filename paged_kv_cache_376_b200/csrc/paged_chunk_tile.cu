@@ -9,9 +9,18 @@
 // it by more than 2^8 (then O and the sum are rescaled).
 //
 // What bounds it: 2 x 64 multiply-adds and one exponential per (row, key).
-// Per SM and clock the tensor core does 4096 multiply-adds and the special
-// function unit 16 exponentials, so a 128 x 128 tile costs 512 clocks of the
-// one and 1024 of the other: the exponentials are the floor.
+// Per SM and clock the tensor core does 4096 multiply-adds (here 2900: 46
+// clocks for a product of N = 64) and the special function unit 16
+// exponentials, so a 128 x 128 tile costs 512 (720) clocks of the one and 1024
+// of the other, 768 with every fourth pair on the FMA units.  Measured: 2250
+// clocks a tile for one query tile alone, 1600 for each of two.  It is the
+// softmax warps' own latency: without nearly all products the step is 3 %
+// shorter, without the exponentials 24 %, and fewer instructions (no maximum),
+// a third of the pairs on the FMA units, or other orders change nothing; two
+// warps per scheduler are what tensor memory (S, P and O of two query tiles)
+// and registers leave room for (four at 96 registers: slower, they spill).
+// 32 decoder prompts over 1500 states: 160 us (400 TFLOP/s, plan and launches
+// included); 256 rows x 5120 keys each: 640 TFLOP/s.
 //
 // Design.
 //  * A plan kernel (one CTA) lists the work: (sequence, block of 256 rows),
@@ -34,7 +43,7 @@
 //    maximum beside it; only where a row's maximum grew by more than 2^8 (and
 //    at a unit's first half) does it move the offset, rescale O and the sum
 //    and exponentiate again from the registers.
-//  * P enters the second product in bf16.  A weight's rounding (2^-9 of it)
+//  * P enters the second product in bf16.  A weight's rounding (up to 2^-8)
 //    averages out over the keys of a row, except where there are few: units
 //    whose first row sees fewer than kExactKeys keys add P's remainder,
 //    P - bf16(P), in a second pass over the tile.
@@ -371,7 +380,7 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr,
 
 // 2^x of a pair on the FMA units: x = n + f, |f| <= 1/2 (n by adding and
 // subtracting 1.5 x 2^23), 2^f by the cubic of least relative error on that
-// range (Remez exchange; 7.5e-5, against the 2^-9 of the bf16 that it becomes),
+// range (Remez exchange; 7.5e-5, against the up to 3.9e-3 of the bf16 that it becomes),
 // 2^n from its exponent bits.  Below 2^-126 it stays there.
 __device__ __forceinline__ float max_nan(float a, float b) {
   float r;

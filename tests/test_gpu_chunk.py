@@ -3,8 +3,14 @@
 Bound (assert_parity): the output's own rounding is at most 2^-8 of it.  The
 weights come from binary32 scores of 64 products (relative error of a weight
 at most 64 x 2^-23 x sum|q k| x scale x log2 e, about 2^-14 here) and enter the
-second product with 16 bits (2^-17); with |v| < 6 that is below 1e-3, the
-absolute part."""
+second product with 16 bits (2^-17) where a block's first row sees fewer than
+512 keys; with |v| < 6 that is below 1e-3, the absolute part.  From 512 keys on
+they enter with 8 bits: an element is off by sum p d v / sum p with |d| <= 2^-8
+(half a step of bf16), independent and evenly spread, so with standard deviation
+at most 2^-8 / sqrt(3) x sqrt(sum p^2 v^2) / sum p.  For normal scores of
+deviation 1 sum p^2 / (sum p)^2 is e / n, so that is at most 2.26e-3 x
+sqrt(e / 512) = 1.6e-4, and 1e-3 is six of them.  Where few keys carry the
+weight, the bound is 2^-8 x sum p |v| / sum p (test_concentrated_weights)."""
 import numpy as np
 import pytest
 import torch
@@ -146,6 +152,36 @@ def test_climbing_maxima(rows):
     for ws in (False, True):
         assert_parity(_call(db, wl.scale, workspace=ws), ref, "climbing",
                       abs_=6 * 2.0 ** -8)
+
+
+@pytest.mark.parametrize("rows,causal", [(8, True), (200, True), (8, False),
+                                         (200, False)])
+def test_concentrated_weights(rows, causal):
+    """Scores of deviation 6 over 2000 keys: a few keys carry each row.  The
+    worst case of 8-bit weights, half a step of bf16, is 2^-8 of the sum of
+    p |v| (taken from the oracle with |V|), beside the output's 2^-8 and the
+    weights' binary32 error: 64 additions x 2^-24 x sum|q k| (about 41) x scale
+    x log2 e (1.08) x ln 2 = 1.2e-4 of p |v|, doubled for the sum: < 2^-10."""
+    lens = [2000, 700]
+    wl = (W.prefill_workload([n - rows for n in lens], [rows] * 2, seed=516,
+                             **_heads(4, 2)) if causal
+          else U.cross_workload(lens, [rows] * 2, 516, **_heads(4, 2)))
+    db = upload(wl)
+    if causal:
+        gpu_append(db)
+        kp, vp = oracle_after_append(wl)
+    else:
+        kp, vp = wl.k_pool, wl.v_pool
+    fn = oracle.paged_prefill if causal else oracle.paged_cross
+    scale = 6 * wl.scale
+    ref, size = (fn(wl.q, wl.query_start_loc, kp, v, wl.block_tables,
+                    wl.context_lens, scale)
+                 for v in (vp, vp & np.uint16(0x7fff)))
+    for ws in (False, True):
+        got = W.bf16_to_f64(bf16_bits(_call(db, scale, causal, workspace=ws)))
+        bound = 2.0 ** -8 * np.abs(ref) + (2.0 ** -8 + 2.0 ** -10) * size
+        assert (np.abs(got - ref) <= bound).all()
+    assert err_word(db) == 0
 
 
 def test_rows_behind_the_last_sequence_stay():
