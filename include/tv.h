@@ -170,7 +170,8 @@ tv_status tv_kv_append_rope(const void* k_new, const void* v_new,
  * [0, rope_max_position) enters unrotated as a whole and flags
  * TV_DEVERR_BAD_POSITION, and so does every token when pair_axis names no
  * axis.  Two tokens mapped to one slot race, as in tv_kv_append.  q_out may
- * be q itself (rows contiguous); it overlaps nothing else.
+ * be q itself (rows contiguous); if it overlaps q, k_new or v_new in any other
+ * way, the call is refused (TV_ERR_INVALID_ARG).
  */
 tv_status tv_kv_append_mrope(void* q_out, const void* q, int64_t q_stride,
                              const void* k_new, int64_t k_stride,
@@ -402,7 +403,8 @@ tv_status tv_prefill_workspace_size(int num_seqs, int max_query_len,
  * one token per step or a prompt; this call serves what lies between, where a
  * prefill tile would be mostly padding and one CTA would walk a long context
  * alone.
- *   out              [total_rows][num_q_heads][head_dim] bf16, written
+ *   out              [total_rows][num_q_heads][head_dim] bf16, written; apart
+ *                    from q (TV_ERR_INVALID_ARG otherwise)
  *   q                [total_rows][num_q_heads][head_dim] bf16
  *   num_query_rows   total_rows (the row count of q and out)
  *   query_start_loc  [num_seqs + 1] int32, non-decreasing, [0] == 0,

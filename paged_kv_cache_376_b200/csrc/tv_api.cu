@@ -114,6 +114,12 @@ tv_status query_tensor_map(CUtensorMap* map, const void* q, int64_t rows,
   return TV_OK;
 }
 
+bool overlap(const void* a, int64_t a_bytes, const void* b, int64_t b_bytes) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a);
+  const uintptr_t y = reinterpret_cast<uintptr_t>(b);
+  return x < y + (uintptr_t)b_bytes && y < x + (uintptr_t)a_bytes;
+}
+
 tv_status check_attention_shape(int num_q_heads, int num_kv_heads,
                                 int head_dim, int page_size) {
   if (head_dim != kHeadDim || !page_size_ok(page_size))
@@ -217,6 +223,16 @@ tv_status tv_kv_append_mrope(void* q_out, const void* q, int64_t q_stride,
   if ((q && (q_stride < q_row || q_stride % 8)) || k_stride < kv_row ||
       k_stride % 8 || v_stride < kv_row || v_stride % 8)
     return TV_ERR_INVALID_ARG;
+  if (q) {
+    // q_out is q itself, row for row, or apart from everything that is read
+    const int64_t bytes = num_tokens * q_row * 2;
+    auto reads = [&](const void* p, int64_t stride, int64_t row) {
+      return overlap(q_out, bytes, p, ((num_tokens - 1) * stride + row) * 2);
+    };
+    if ((!(q_out == q && q_stride == q_row) && reads(q, q_stride, q_row)) ||
+        reads(k_new, k_stride, kv_row) || reads(v_new, v_stride, kv_row))
+      return TV_ERR_INVALID_ARG;
+  }
   tv::MropeArgs a{};
   a.q_out = static_cast<__nv_bfloat16*>(q_out);
   a.q = static_cast<const __nv_bfloat16*>(q);
@@ -873,6 +889,8 @@ static tv_status chunk_common(void* out, const void* q, int64_t num_query_rows,
   if (!aligned16(out) || !aligned16(q) || !aligned16(k_pool) ||
       !aligned16(v_pool))
     return TV_ERR_INVALID_ARG;
+  const int64_t q_bytes = num_query_rows * num_q_heads * head_dim * 2;
+  if (overlap(out, q_bytes, q, q_bytes)) return TV_ERR_INVALID_ARG;
   const int shift = group_shift_of(group);
   ChunkWorkspace ws{};
   if (workspace) {

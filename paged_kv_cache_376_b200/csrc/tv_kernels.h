@@ -32,17 +32,24 @@ template <auto kKernel, typename... Args>
 cudaError_t launch_kernel(dim3 grid, int threads, int bytes, bool overlap,
                           cudaStream_t stream, Args... args) {
   static std::atomic<uint64_t> raised;
+  uint64_t bit = 0;
+  bool known = true;
   if (bytes > 48 * 1024) {
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
-    const uint64_t bit = dev < 64 ? 1ull << dev : 0;
-    if (!(raised.load(std::memory_order_relaxed) & bit)) {
-      e = cudaFuncSetAttribute(
-          kKernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
-      if (e != cudaSuccess) return e;
-      raised.fetch_or(bit, std::memory_order_relaxed);
-    }
+    bit = dev < 64 ? 1ull << dev : 0;
+    known = raised.load(std::memory_order_relaxed) & bit;
+  }
+  auto raise = [&]() {
+    cudaError_t e = cudaFuncSetAttribute(
+        kKernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e == cudaSuccess) raised.fetch_or(bit, std::memory_order_relaxed);
+    return e;
+  };
+  if (!known) {
+    cudaError_t e = raise();
+    if (e != cudaSuccess) return e;
   }
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = grid;
@@ -54,7 +61,14 @@ cudaError_t launch_kernel(dim3 grid, int threads, int bytes, bool overlap,
   attr.val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = &attr;
   cfg.numAttrs = overlap ? 1 : 0;
-  return cudaLaunchKernelEx(&cfg, kKernel, args...);
+  cudaError_t e = cudaLaunchKernelEx(&cfg, kKernel, args...);
+  if (e == cudaErrorInvalidValue && bit) {
+    // a device that was reset has forgotten the limit
+    (void)cudaGetLastError();
+    e = raise();
+    if (e == cudaSuccess) e = cudaLaunchKernelEx(&cfg, kKernel, args...);
+  }
+  return e;
 }
 
 struct DecodeArgs {

@@ -143,10 +143,11 @@ def lib():
 
 P = ctypes.c_void_p(0x10000)
 ODD = ctypes.c_void_p(0x10008)
+FAR = ctypes.c_void_p(0x10000000)
 
 
 def _chunk(lib, name, **kw):
-    a = dict(out=P, q=P, rows=8, qsl=P, k=P, v=P, bt=P, mb=4, ctx=P, b=1,
+    a = dict(out=FAR, q=P, rows=8, qsl=P, k=P, v=P, bt=P, mb=4, ctx=P, b=1,
              maxq=8, hq=32, hkv=8, d=64, ps=16, np=10, scale=0.125, ws=None,
              ws_bytes=0)
     a.update(kw)
@@ -168,7 +169,9 @@ def test_chunk_refusals(lib, name):
                dict(scale=-0.1), dict(scale=float("inf")), dict(q=None),
                dict(out=None), dict(qsl=None), dict(k=None), dict(v=None),
                dict(bt=None), dict(ctx=None), dict(q=ODD), dict(out=ODD),
-               dict(k=ODD), dict(v=ODD), dict(ws=ODD, ws_bytes=1 << 30)):
+               dict(k=ODD), dict(v=ODD), dict(ws=ODD, ws_bytes=1 << 30),
+               dict(out=P), dict(out=ctypes.c_void_p(0x10000 + 4096 * 8 - 16)),
+               dict(q=ctypes.c_void_p(0x10000000 + 16))):
         assert _chunk(lib, name, **kw) == 1, kw
     for kw in (dict(b=0), dict(rows=0), dict(maxq=0)):
         assert _chunk(lib, name, **kw) == 0, kw
@@ -186,7 +189,7 @@ def test_chunk_workspace_size_refusals(lib):
 
 def test_mrope_refusals(lib):
     def call(**kw):
-        a = dict(qo=P, q=P, qs=2048, k=P, ks=512, v=P, vs=512, slots=P, pos=P,
+        a = dict(qo=FAR, q=P, qs=2048, k=P, ks=512, v=P, vs=512, slots=P, pos=P,
                  axes=3, axis=P, t=4, kp=P, vp=P, np=10, hq=32, hkv=8, d=64,
                  ps=16, tab=P, npos=8)
         a.update(kw)
@@ -205,7 +208,9 @@ def test_mrope_refusals(lib):
                dict(npos=0), dict(q=ODD), dict(qo=ODD), dict(k=ODD),
                dict(v=ODD), dict(kp=ODD), dict(vp=ODD), dict(tab=ODD),
                dict(qs=2047), dict(qs=2052), dict(ks=504), dict(ks=516),
-               dict(vs=504), dict(vs=517), dict(ks=0)):
+               dict(vs=504), dict(vs=517), dict(ks=0),
+               dict(q=FAR, qs=2056), dict(k=FAR), dict(v=FAR),
+               dict(q=ctypes.c_void_p(0x10000010))):
         assert call(**kw) == 1, kw
     assert call(t=0) == 0
 
