@@ -30,9 +30,8 @@
 // averages out over the keys of a row, except where there are few: blocks
 // whose first row sees fewer than kChunkExactKeys keys add P's remainder,
 // P - bf16(P), with a second product, as the decode and the prefill always do.
+#include "tv_chunk.cuh"
 #include "tv_decode.cuh"
-#include "tv_device.cuh"
-#include "tv_kernels.h"
 
 namespace tv {
 namespace {
@@ -368,6 +367,14 @@ struct Joined {
     y.z = fmaf(v.z, f, y.z);
     y.w = fmaf(v.w, f, y.w);
   }
+  // a larger offset for what was added so far
+  __device__ __forceinline__ void raise(float m) {
+    const float f = m == M ? 1.f : fast_exp2(M - m);
+    M = m;
+    L *= f;
+    x = make_float4(x.x * f, x.y * f, x.z * f, x.w * f);
+    y = make_float4(y.x * f, y.y * f, y.z * f, y.w * f);
+  }
   __device__ __forceinline__ void write(__nv_bfloat16* row, int k) const {
     const float inv = L == 0.f ? 0.f : 1.f / L;   // NaN scores stay NaN
     *reinterpret_cast<uint2*>(row + 4 * k) = make_uint2(
@@ -654,6 +661,62 @@ __device__ __forceinline__ void compute_barrier() {
   asm volatile("bar.sync 1, %0;" ::"n"(kW * 32) : "memory");
 }
 
+// Joins the parts of the blocks that the tile kernel cut along the keys: a warp
+// takes 8 dims of 32 rows (a lane each) of one query tile and KV head.
+template <bool kCausal>
+__device__ __forceinline__ void join_tiles(const ChunkArgs& a, int warp,
+                                           int warps, int lane) {
+  const int Hkv = a.num_kv_heads;
+  const int tasks = __ldcg(&a.plan->joins) * Hkv * 2 * 4 * 8;
+  for (int i = warp; i < tasks; i += warps) {
+    const int dims = i & 7, quarter = (i >> 3) & 3, t = (i >> 5) & 1;
+    const int kvh = (i >> 6) % Hkv;
+    const int4 e = __ldcg(a.plan_joins + (i >> 6) / Hkv);
+    TileBlock b;
+    tile_block<kCausal>(a, e.x, e.y, &b);
+    const int r = quarter * 32 + lane;           // row of the query tile
+    const int row = t * 128 + r;                 // row of the block
+    const float* part0 = a.tile_parts +
+                         ((size_t)e.z * Hkv + kvh) * kTilePartFloats +
+                         t * (kTilePartFloats / 2);
+    const size_t step = (size_t)Hkv * kTilePartFloats;
+    Joined j;
+    for (int k0 = 0; k0 < e.w; k0 += 8) {
+      float m8[8], l8[8];
+      float4 x8[8], y8[8];
+      float top = j.M;
+#pragma unroll
+      for (int q = 0; q < 8; ++q) {
+        m8[q] = -INFINITY;
+        l8[q] = 0.f;
+        x8[q] = y8[q] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (k0 + q < e.w) {
+          const float* p = part0 + (k0 + q) * step;
+          const float4* v = reinterpret_cast<const float4*>(p + 256) +
+                            2 * dims * 128 + r;
+          m8[q] = __ldcg(p + r);
+          l8[q] = __ldcg(p + 128 + r);
+          x8[q] = __ldcg(v);
+          y8[q] = __ldcg(v + 128);
+        }
+      }
+#pragma unroll
+      for (int q = 0; q < 8; ++q) top = fmaxf(top, m8[q]);
+      j.raise(top);
+#pragma unroll
+      for (int q = 0; q < 8; ++q) j.add(m8[q], l8[q], x8[q], y8[q]);
+    }
+    if (row < b.tb << a.group_shift) {
+      const float inv = j.L == 0.f ? 0.f : 1.f / j.L;   // NaN scores stay NaN
+      *reinterpret_cast<uint4*>(out_row(a, b.q_row, kvh, row) + 8 * dims) =
+          make_uint4(pack_bf16x2(j.x.x * inv, j.x.y * inv),
+                     pack_bf16x2(j.x.z * inv, j.x.w * inv),
+                     pack_bf16x2(j.y.x * inv, j.y.y * inv),
+                     pack_bf16x2(j.y.z * inv, j.y.w * inv));
+    }
+  }
+}
+
 template <int MB, bool kCausal>
 __global__ void __launch_bounds__((compute_warps(MB) + 1) * 32,
                                   ctas_per_sm(MB))
@@ -718,7 +781,10 @@ __global__ void __launch_bounds__((compute_warps(MB) + 1) * 32,
   line.pre = sm.pre;
   line.B = B;
   line.W = sm.pre[B];
-  line.NG = min((int)gridDim.x / Hkv, max(line.W / kMinChunkBlocks, sm.items));
+  // A range worth a CTA: more parts of one sequence shorten its ranges but are
+  // joined by one CTA, so ranges grow with the root of the whole.
+  const int least = min(64, max(kMinChunkBlocks, (int)(0.6f * sqrtf(line.W))));
+  line.NG = min((int)gridDim.x / Hkv, max(line.W / least, sm.items));
   const int W = line.W, NG = line.NG;
   const int grp = blockIdx.x / Hkv;
   const int head = blockIdx.x - grp * Hkv;
@@ -929,20 +995,53 @@ __global__ void __launch_bounds__((compute_warps(MB) + 1) * 32,
         };
         int qs, T, ctx;
         sequence_rows<kCausal>(a, s, false, &qs, &T, &ctx);
-        for (int row = r16; row < T << a.group_shift; row += kW * 4) {
-          Joined j;
-#pragma unroll 4
-          for (int k = 0; k < parts.n; ++k)
-            j.M = fmaxf(j.M, __ldcg(part_of(k) + row));
-#pragma unroll 4
-          for (int k = 0; k < parts.n; ++k) {
-            const float* q = part_of(k);
-            const float4* v = reinterpret_cast<const float4*>(
-                q + 2 * kChunkPartRows + row * kD + 4 * k8);
-            j.add(__ldcg(q + row), __ldcg(q + kChunkPartRows + row),
-                  __ldcg(v), __ldcg(v + 8));
+          // warp w joins parts w, w + kW, ... of 4 rows at a time (eight of them
+        // in flight), then the warps' results as after a range
+        const int jr = lane >> 3;
+        for (int row0 = 0; row0 < T << a.group_shift; row0 += 16) {
+#pragma unroll 1
+          for (int g = 0; g < 16; g += 4) {
+            const int row = min(row0 + g + jr, kChunkPartRows - 1);
+            Joined j;
+            for (int k0 = warp; k0 < parts.n; k0 += 8 * kW) {
+              float m8[8], l8[8];
+              float4 x8[8], y8[8];
+              float top = j.M;
+#pragma unroll
+              for (int e = 0; e < 8; ++e) {
+                const int k = k0 + e * kW;
+                m8[e] = -INFINITY;
+                l8[e] = 0.f;
+                x8[e] = y8[e] = make_float4(0.f, 0.f, 0.f, 0.f);
+                if (k < parts.n) {
+                  const float* q = part_of(k);
+                  const float4* v = reinterpret_cast<const float4*>(
+                      q + 2 * kChunkPartRows + row * kD + 4 * k8);
+                  m8[e] = __ldcg(q + row);
+                  l8[e] = __ldcg(q + kChunkPartRows + row);
+                  x8[e] = __ldcg(v);
+                  y8[e] = __ldcg(v + 8);
+                }
+              }
+#pragma unroll
+              for (int e = 0; e < 8; ++e) top = fmaxf(top, m8[e]);
+              j.raise(top);
+#pragma unroll
+              for (int e = 0; e < 8; ++e) j.add(m8[e], l8[e], x8[e], y8[e]);
+            }
+            if (k8 == 0) {
+              sm.cb.m[warp][g + jr] = j.M;
+              sm.cb.l[warp][g + jr] = j.L;
+            }
+            float* acc = sm.cb.acc[warp][g + jr];
+            *reinterpret_cast<float4*>(acc + 4 * k8) = j.x;
+            *reinterpret_cast<float4*>(acc + 32 + 4 * k8) = j.y;
           }
-          j.write(out_row(a, qs, head, row), k8);
+          compute_barrier<kW>();
+          if (r16 < 16 && row0 + r16 < T << a.group_shift)
+            join_warps(sm.cb, r16, k8)
+                .write(out_row(a, qs, head, row0 + r16), k8);
+          compute_barrier<kW>();
         }
         if (threadIdx.x == 0) a.ws_counters[(size_t)s * Hkv + head] = 0;
       }
@@ -950,7 +1049,11 @@ __global__ void __launch_bounds__((compute_warps(MB) + 1) * 32,
     if (failed && lane == 0) flag_error(a.err, DEVERR_TIMEOUT);
   }
   // the rows of the tile kernel are written when this kernel ends
-  if (a.tile_ctas) wait_for_last_kernel();
+  if (a.tile_ctas) {
+    wait_for_last_kernel();
+    join_tiles<kCausal>(a, blockIdx.x * (kBalancedThreads / 32) + warp,
+                        gridDim.x * (kBalancedThreads / 32), lane);
+  }
 }
 
 template <int MB>

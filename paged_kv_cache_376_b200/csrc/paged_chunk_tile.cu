@@ -51,11 +51,11 @@
 //    diagonal or the end, warp 0 zeroes the V rows behind the last key and
 //    takes infinities and NaNs out of V; it notes per dim the first key
 //    that held one, and rows that see that key get NaN there.
-//  * A cut block leaves (m, l, O) per range in the workspace; the CTA that
-//    completes its counter joins them in the order of the keys.
+//  * A cut block leaves (m, l, O) per range in the workspace; the streaming
+//    kernel that follows joins them, in the order of the keys, with all its
+//    warps (one CTA joining the 130 parts of one long sequence took 110 us).
 //  * Every wait is bounded (2 s).
-#include "tv_device.cuh"
-#include "tv_kernels.h"
+#include "tv_chunk.cuh"
 
 namespace tv {
 namespace {
@@ -78,41 +78,12 @@ constexpr int kSCol = 0;                  // S, then P, in buffer b of query
 constexpr int kOCol = 384;                // O of tile t: [384 + 64 t, +64)
 constexpr float kLazy = 8.f;              // log2 of the growth allowed
 constexpr int kExactKeys = kChunkExactKeys;   // see the file comment
-constexpr int kMinTiles = 4;              // key tiles worth a unit of their own
+constexpr int kMinTiles = 8;              // key tiles worth a unit of their own
 
 constexpr uint32_t kIdescQK = idesc_bf16_f32(kBM, kHalf, false);
 constexpr uint32_t kIdescPV = idesc_bf16_f32(kBM, kD, true);
 
 // ---- plan -----------------------------------------------------------------------
-// The key tiles of a block, from the rows it covers.
-struct Block {
-  int q_row;            // first query row in q / out
-  int tb;               // query rows
-  int first_limit;      // last key that the first row sees
-  int key_end;          // keys that some row sees: [0, key_end)
-};
-
-template <bool kCausal>
-__device__ __forceinline__ bool tile_block(const ChunkArgs& a, int seq,
-                                           int blk, Block* b) {
-  const int qs = a.query_start_loc[seq];
-  const int T = a.query_start_loc[seq + 1] - qs;
-  const int cap = a.max_blocks_per_seq * (kPS << a.page_shift);
-  const int ctx = min(max(a.context_lens[seq], 0), cap);
-  // what is out of range is flagged by the streaming kernel of this call
-  if (T <= a.stream_rows || T > a.max_query_len || qs < 0 ||
-      (int64_t)qs + T > a.num_query_rows || (kCausal && T > ctx))
-    return false;
-  const int rows = 2 * kBM >> a.group_shift;
-  const int t0 = blk * rows;
-  if (t0 >= T) return false;
-  b->q_row = qs + t0;
-  b->tb = min(rows, T - t0);
-  b->first_limit = kCausal ? ctx - T + t0 : ctx - 1;
-  b->key_end = kCausal ? b->first_limit + b->tb : ctx;
-  return true;
-}
-
 constexpr int kPlanThreads = 1024;
 constexpr int kBuckets = kPlanThreads;     // costs above share the top
 
@@ -122,7 +93,7 @@ __global__ void __launch_bounds__(kPlanThreads, 1)
   __shared__ int slot[kBuckets];          // histogram, then next free position
   __shared__ int warp_sum[32];
   __shared__ unsigned long long total;
-  __shared__ int parts;
+  __shared__ int parts, joins;
   let_next_kernel_start();
   const int nblk = chunk_tile_blocks(a.max_query_len, a.group_shift);
   const int n_items = a.num_seqs * nblk;
@@ -130,23 +101,24 @@ __global__ void __launch_bounds__(kPlanThreads, 1)
   if (threadIdx.x == 0) {
     total = 0;
     parts = 0;
+    joins = 0;
   }
-  auto tiles_of = [&](int item, Block* b) {
+  auto tiles_of = [&](int item, TileBlock* b) {
     return tile_block<kCausal>(a, item / nblk, item % nblk, b)
                ? (b->key_end + kBN - 1) / kBN
                : -1;
   };
   // the thread's first item stays in registers for the further passes
-  Block b0{};
+  TileBlock b0{};
   const int n0 = (int)threadIdx.x < n_items ? tiles_of(threadIdx.x, &b0) : -1;
-  auto again = [&](int item, Block* b) {
+  auto again = [&](int item, TileBlock* b) {
     if (item == (int)threadIdx.x) {
       *b = b0;
       return n0;
     }
     return tiles_of(item, b);
   };
-  Block b;
+  TileBlock b;
   long long mine = max(0, n0);
   for (int i = threadIdx.x + kPlanThreads; i < n_items; i += kPlanThreads)
     mine += max(0, tiles_of(i, &b));
@@ -163,7 +135,7 @@ __global__ void __launch_bounds__(kPlanThreads, 1)
   };
   // key tiles, two thirds of them where there is one query tile
   const int per = kBM >> a.group_shift;
-  auto cost = [&](const Block& b, int n) {
+  auto cost = [&](const TileBlock& b, int n) {
     return min(b.tb > per ? 3 * n : 2 * n, kBuckets - 1);
   };
   auto edge = [](int n, int k, int of) { return (int)((long long)n * k / of); };
@@ -208,6 +180,9 @@ __global__ void __launch_bounds__(kPlanThreads, 1)
     if (n < 0) continue;
     const int of = cuts_of(n);
     const int base = of > 1 ? atomicAdd(&parts, of) : -1;
+    if (of > 1)
+      a.plan_joins[atomicAdd(&joins, 1)] =
+          make_int4(i / nblk, i % nblk, base, of);
     for (int k = 0; k < of; ++k) {
       const int k0 = edge(n, k, of), k1 = edge(n, k + 1, of);
       ChunkEntry e;
@@ -222,13 +197,15 @@ __global__ void __launch_bounds__(kPlanThreads, 1)
       a.plan_entries[atomicAdd(&slot[cost(b, k1 - k0)], 1)] = e;
     }
   }
+  __syncthreads();
+  if (threadIdx.x == 0) a.plan->joins = joins;
 }
 
 // ---- the kernel ------------------------------------------------------------------------
 // A unit: a plan entry for one KV head, and what follows from it.
 struct Unit {
   ChunkEntry e;
-  Block b;
+  TileBlock b;
   int kvh;
   int n[2];        // key tiles of query tile 0 / 1, from e.tile0 on
   int n_tiles;     // key tiles loaded
@@ -246,7 +223,7 @@ struct TileSmem {
   uint64_t kv_full[kST], kv_empty[kST];
   uint64_t v_ready[kST];     // V of an edge tile is clean
   uint64_t s_full[2][kBuf], p_full[2][kBuf], o_done[2][kBuf];
-  uint64_t o_free[2], part_in[2], part_out[2];     // [query tile]
+  uint64_t o_free[2];                              // [query tile]
   uint64_t drain[3];
   uint32_t tmem_base;
   uint32_t bad_pages[kST];
@@ -254,7 +231,6 @@ struct TileSmem {
   int32_t poison[2][kD];     // first key with a non-finite V
   int32_t poisoned[2];       // any of them
   int32_t bad_unit[2];       // a page of the unit so far was bad
-  int32_t last[2];
   Unit unit[2];              // [unit parity]
 };
 
@@ -468,8 +444,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         mbar_init(smem_u32(&sm.p_full[i][k]), 4);
         mbar_init(smem_u32(&sm.o_done[i][k]), 1);
       }
-      mbar_init(smem_u32(&sm.part_in[i]), 4);
-      mbar_init(smem_u32(&sm.part_out[i]), 1);
     }
     for (int i = 0; i < kST; ++i) {
       mbar_init(smem_u32(&sm.kv_full[i]), 1);
@@ -730,7 +704,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const float cs = a.scale_log2;
     const float2 cs2 = make_float2(cs, cs);
     bool ok = true;
-    uint32_t it = 0, joins = 0;
+    uint32_t it = 0;
     Turn h;
     // O holds every half handed over so far (there is one)
     auto o_ready = [&]() {
@@ -896,14 +870,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!wait_warp(&sm.clean[ub], (round >> 1) & 1)) ok = false;
       const bool poisoned = sm.poisoned[ub] != 0;
       const int parts = u.e.parts;
-      const size_t slot0 = (size_t)u.e.part_base * a.num_kv_heads + u.kvh;
       // a part: m, l, then O as [dim / 4][row] float4, so that a warp's
       // accesses are contiguous
-      auto part = [&](int k) {
-        return a.tile_parts +
-               (slot0 + (size_t)k * a.num_kv_heads) * kTilePartFloats +
-               t * (kTilePartFloats / 2);
-      };
+      float* part =
+          a.tile_parts +
+          ((size_t)(u.e.part_base + u.e.part) * a.num_kv_heads + u.kvh) *
+              kTilePartFloats +
+          t * (kTilePartFloats / 2);
       uint4* dst = reinterpret_cast<uint4*>(
           a.out + ((size_t)(u.b.q_row + t * per + qi) * a.num_q_heads +
                    (u.kvh << a.group_shift) + hh) * kD);
@@ -935,7 +908,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (sm.poison[ub][d0 + d] <= limit) o[d] = NAN;
         }
         if (parts > 1) {
-          float4* to = reinterpret_cast<float4*>(part(u.e.part) + 2 * kBM) +
+          float4* to = reinterpret_cast<float4*>(part + 2 * kBM) +
                        d0 / 4 * kBM + r;
 #pragma unroll
           for (int d = 0; d < 8; ++d)
@@ -951,57 +924,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (lane == 0) mbar_arrive(smem_u32(&sm.o_free[t]));
       }
       if (parts > 1) {
-        __stcg(part(u.e.part) + r, m_run);
-        __stcg(part(u.e.part) + kBM + r, l_run);
-        // the four warps' stores, then one count for the part
-        __syncwarp();
-        if (lane == 0) mbar_arrive(smem_u32(&sm.part_in[t]));
-        if (quarter == 0 && lane == 0) {
-          bool last = false;
-          if (mbar_wait(smem_u32(&sm.part_in[t]), joins & 1)) {
-            int32_t* counter = a.tile_counters + 2 * slot0 + t;
-            __threadfence();
-            last = atomicAdd(counter, 1) == parts - 1;
-            if (last) *counter = 0;
-            __threadfence();
-          }
-          sm.last[t] = last;
-          mbar_arrive(smem_u32(&sm.part_out[t]));
-        }
-        if (!wait_warp(&sm.part_out[t], joins & 1)) ok = false;
-        ++joins;
-        if (ok && sm.last[t]) {
-          float M = -INFINITY, L = 0.f;
-          for (int k = 0; k < parts; ++k) M = fmaxf(M, __ldcg(part(k) + r));
-          // equal offsets first: -inf must not become NaN
-          auto factor = [&](int k) {
-            const float m = __ldcg(part(k) + r);
-            return m == M ? 1.f : fast_exp2(m - M);
-          };
-          for (int k = 0; k < parts; ++k)
-            L = fmaf(__ldcg(part(k) + kBM + r), factor(k), L);
-#pragma unroll 1
-          for (int d0 = 0; d0 < kD; d0 += 32) {
-            float o[32];
-#pragma unroll
-            for (int d = 0; d < 32; ++d) o[d] = 0.f;
-            for (int k = 0; k < parts; ++k) {
-              const float f = factor(k);
-              const float4* from =
-                  reinterpret_cast<const float4*>(part(k) + 2 * kBM) +
-                  d0 / 4 * kBM + r;
-#pragma unroll
-              for (int d = 0; d < 8; ++d) {
-                const float4 x = __ldcg(from + d * kBM);
-                o[4 * d] = fmaf(x.x, f, o[4 * d]);
-                o[4 * d + 1] = fmaf(x.y, f, o[4 * d + 1]);
-                o[4 * d + 2] = fmaf(x.z, f, o[4 * d + 2]);
-                o[4 * d + 3] = fmaf(x.w, f, o[4 * d + 3]);
-              }
-            }
-            if (real) write32(o, d0, L == 0.f ? 0.f : 1.f / L);
-          }
-        }
+        __stcg(part + r, m_run);
+        __stcg(part + kBM + r, l_run);
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(smem_u32(&sm.q_empty[ub]));

@@ -813,7 +813,7 @@ tv_status tv_paged_prefill(void* out, const void* q, int64_t num_query_rows,
 static int chunk_ctas() { return device_sms() * tv::kChunkCtasPerSm; }
 
 struct ChunkWorkspace {
-  size_t tile_counters, parts, plan, entries, tile_parts, bytes;
+  size_t parts, plan, joins, entries, tile_parts, bytes;
 };
 
 static ChunkWorkspace chunk_workspace(int num_seqs, int max_query_len,
@@ -823,11 +823,11 @@ static ChunkWorkspace chunk_workspace(int num_seqs, int max_query_len,
   const bool tiles =
       ((int64_t)max_query_len << group_shift) > tv::kChunkPartRows;
   ChunkWorkspace w;
-  w.tile_counters = counters_bytes(num_seqs, num_kv_heads);
-  w.parts = w.tile_counters + (tiles ? up(sms * 4 * 2 * sizeof(int32_t)) : 0);
+  w.parts = counters_bytes(num_seqs, num_kv_heads);
   w.plan = w.parts + up((size_t)chunk_ctas() * 2 * tv::kChunkPartFloats *
                         sizeof(float));
-  w.entries = w.plan + (tiles ? 256 : 0);
+  w.joins = w.plan + (tiles ? 256 : 0);
+  w.entries = w.joins + (tiles ? up(4 * sms * sizeof(int4)) : 0);
   // every block once, and the further parts of those that are cut
   const size_t n = (size_t)num_seqs *
                        tv::chunk_tile_blocks(max_query_len, group_shift) +
@@ -937,7 +937,7 @@ static tv_status chunk_common(void* out, const void* q, int64_t num_query_rows,
       a.tile_ctas = device_sms();
       a.plan = reinterpret_cast<tv::ChunkPlan*>(base + ws.plan);
       a.plan_entries = reinterpret_cast<tv::ChunkEntry*>(base + ws.entries);
-      a.tile_counters = reinterpret_cast<int32_t*>(base + ws.tile_counters);
+      a.plan_joins = reinterpret_cast<int4*>(base + ws.joins);
       a.tile_parts = reinterpret_cast<float*>(base + ws.tile_parts);
       CUtensorMap tq;
       st = query_tensor_map(&tq, q, num_query_rows, num_q_heads, group,

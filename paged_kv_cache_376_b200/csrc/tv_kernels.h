@@ -258,6 +258,7 @@ struct ChunkEntry {              // work of the tile kernel, for every KV head
 struct ChunkPlan {
   int32_t entries;
   int32_t next;                  // unit (entry x KV head) to be taken next
+  int32_t joins;                 // cut blocks
 };
 struct ChunkArgs {
   __nv_bfloat16* out;            // [rows][Hq][D]
@@ -286,7 +287,7 @@ struct ChunkArgs {
   int tile_ctas;
   ChunkPlan* plan;
   ChunkEntry* plan_entries;
-  int32_t* tile_counters;        // [4 tile_ctas][2], zero between calls
+  int4* plan_joins;              // cut blocks: sequence, block, part_base, parts
   float* tile_parts;             // [4 tile_ctas][kTilePartFloats]
 };
 constexpr int kMaxChunkSeqs = 1024;     // prefix sums live in shared memory
