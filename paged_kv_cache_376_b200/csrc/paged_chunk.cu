@@ -995,10 +995,27 @@ __global__ void __launch_bounds__((compute_warps(MB) + 1) * 32,
         };
         int qs, T, ctx;
         sequence_rows<kCausal>(a, s, false, &qs, &T, &ctx);
-          // warp w joins parts w, w + kW, ... of 4 rows at a time (eight of them
-        // in flight), then the warps' results as after a range
+          // a few parts: a thread joins 8 dims of its rows
+        const bool few = parts.n <= 8;
+        for (int row = r16; few && row < T << a.group_shift; row += kW * 4) {
+          Joined j;
+#pragma unroll 4
+          for (int k = 0; k < parts.n; ++k)
+            j.M = fmaxf(j.M, __ldcg(part_of(k) + row));
+#pragma unroll 4
+          for (int k = 0; k < parts.n; ++k) {
+            const float* q = part_of(k);
+            const float4* v = reinterpret_cast<const float4*>(
+                q + 2 * kChunkPartRows + row * kD + 4 * k8);
+            j.add(__ldcg(q + row), __ldcg(q + kChunkPartRows + row),
+                  __ldcg(v), __ldcg(v + 8));
+          }
+          j.write(out_row(a, qs, head, row), k8);
+        }
+        // many: warp w joins parts w, w + kW, ... of 4 rows at a time (eight of
+        // them in flight), then the warps' results as after a range
         const int jr = lane >> 3;
-        for (int row0 = 0; row0 < T << a.group_shift; row0 += 16) {
+        for (int row0 = 0; !few && row0 < T << a.group_shift; row0 += 16) {
 #pragma unroll 1
           for (int g = 0; g < 16; g += 4) {
             const int row = min(row0 + g + jr, kChunkPartRows - 1);
