@@ -782,7 +782,9 @@ __global__ void __launch_bounds__((compute_warps(MB) + 1) * 32,
   line.B = B;
   line.W = sm.pre[B];
   // A range worth a CTA: more parts of one sequence shorten its ranges but are
-  // joined by one CTA, so ranges grow with the root of the whole.
+  // joined by one CTA, so ranges grow with the root of the whole (one KV head, 31
+  // and 47 rows over 90,063 and 42,422 tokens: 242 us with up to 375 parts of 16
+  // blocks joined thread by thread, now 60).
   const int least = min(64, max(kMinChunkBlocks, (int)(0.6f * sqrtf(line.W))));
   line.NG = min((int)gridDim.x / Hkv, max(line.W / least, sm.items));
   const int W = line.W, NG = line.NG;

@@ -53,7 +53,8 @@
 //    that held one, and rows that see that key get NaN there.
 //  * A cut block leaves (m, l, O) per range in the workspace; the streaming
 //    kernel that follows joins them, in the order of the keys, with all its
-//    warps (one CTA joining the 130 parts of one long sequence took 110 us).
+//    warps (joined by one CTA each, one KV head's 80 and 197 rows over 53,287
+//    and 28,329 tokens took 172 us, most of it the join; now 54).
 //  * Every wait is bounded (2 s).
 #include "tv_chunk.cuh"
 
@@ -207,7 +208,7 @@ struct Unit {
   ChunkEntry e;
   TileBlock b;
   int kvh;
-  int n[2];        // key tiles of query tile 0 / 1, from e.tile0 on
+  int n[2];        // halves of key tiles of query tile 0 / 1, from e.tile0 on
   int n_tiles;     // key tiles loaded
   int edge0;       // first key tile with a key that some row does not see
   int live;        // 0: no more units
@@ -265,7 +266,8 @@ __device__ __forceinline__ void unit_at(const ChunkArgs& a, int i, int n_units,
     const int keys = rows <= 0 ? 0
                      : kCausal ? u->b.first_limit + t * per + rows
                                : u->b.key_end;
-    u->n[t] = max(0, min((keys + kBN - 1) / kBN, u->e.tile1) - u->e.tile0);
+    u->n[t] = max(0, min((keys + kHalf - 1) / kHalf, 2 * u->e.tile1) -
+                         2 * u->e.tile0);
   }
   u->n_tiles = u->e.tile1 - u->e.tile0;
   u->edge0 = max(0, u->b.first_limit + 1) / kBN;
@@ -606,7 +608,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int half = 0; half < 2; ++half)
 #pragma unroll
             for (int t = 0; t < 2; ++t) {
-              if (!ok || j >= (t ? n1 : n0)) continue;
+              if (!ok || 2 * j + half >= (t ? n1 : n0)) continue;
               Turn& h = turn[t];
               // P.V of the buffer's last half has read it (true at first)
               if (!wait_warp(&sm.o_done[t][h.b], h.parity ^ 1)) {
@@ -650,7 +652,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             v_uses ^= 1u << st;
           }
-          if (j >= n) {
+          if (2 * j >= n) {
             if (leader) mbar_arrive(smem_u32(&sm.kv_empty[st]));
             __syncwarp();
             continue;
@@ -658,6 +660,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           const uint32_t v_lo = (uint32_t)dv + st * (kTileBytes >> 4);
 #pragma unroll
           for (int half = 0; half < 2; ++half) {
+            if (2 * j + half >= n) continue;
             if (!ok || !wait_warp(&sm.p_full[t][h.b], h.parity)) {
               ok = false;
               continue;
@@ -738,7 +741,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       //      first, move the offset (rescaling O and the sum) and
       //      exponentiate from the registers (again).  The loop's scalar code
       //      is kept short: it costs as much time as the exponentials ------------
-      const int halves = ok ? 2 * n : 0;
+      const int halves = ok ? n : 0;
       const int plain = exact ? 0 : (tile_limit + 1 - tile0 * kBN) / kHalf;
       volatile const int32_t* bad_unit = &sm.bad_unit[ub];
 #pragma unroll 1

@@ -121,6 +121,20 @@ def test_long_contexts_split_over_keys(lens, rows):
     assert err_word(db) == 0
 
 
+@pytest.mark.parametrize("rows,group", [(1, 1), (5, 4), (29, 1), (60, 1),
+                                        (90, 4)])
+def test_one_kv_head_in_many_parts(rows, group):
+    """One long sequence spread over the whole GPU beside a short one: more
+    parts than a warp joins at once, in both kernels."""
+    lens = [60000, 130]
+    wl, db, ref = _chunk([n - rows for n in lens], [rows] * 2, 517,
+                         num_q_heads=group, num_kv_heads=1)
+    a = _call(db, wl.scale)
+    assert_parity(a, ref, "many parts")
+    assert torch.equal(a, _call(db, wl.scale))
+    assert err_word(db) == 0
+
+
 @pytest.mark.parametrize("page_size", [16, 32])
 @pytest.mark.parametrize("group", [1, 2, 4, 8])
 @pytest.mark.parametrize("lens,rows", [
