@@ -414,8 +414,9 @@ tv_status tv_prefill_workspace_size(int num_seqs, int max_query_len,
  *   workspace        NULL (keys are not split), or device memory of at least
  *                    tv_chunk_workspace_size() bytes, 16-byte aligned, zeroed
  *                    once before its first use (every call leaves its
- *                    counters at zero again).  Calls that overlap on the GPU
- *                    need separate workspaces.
+ *                    counters at zero again, except one that flagged
+ *                    TV_DEVERR_TIMEOUT).  Calls that overlap on the GPU need
+ *                    separate workspaces.
  *   workspace_bytes  its size; too small returns TV_ERR_INVALID_ARG
  * A sequence with T_s > C, T_s > max_query_len or rows outside q is flagged
  * TV_DEVERR_BAD_QUERY and skipped.  scale must be positive

@@ -822,8 +822,7 @@ __global__ void __launch_bounds__((compute_warps(MB) + 1) * 32,
         ahead = look_up(i + kLook);
       }
       const int block = __shfl_sync(0xffffffffu, blocks,
-                                    in_look * kW +
-                                        (issuer ? w : 0));
+                                    in_look * kW + (issuer ? w : 0));
       ++in_look;
       const int stage = i % kStages;
       const bool mine = issuer && block != -2;
@@ -997,7 +996,7 @@ __global__ void __launch_bounds__((compute_warps(MB) + 1) * 32,
         };
         int qs, T, ctx;
         sequence_rows<kCausal>(a, s, false, &qs, &T, &ctx);
-          // a few parts: a thread joins 8 dims of its rows
+        // a few parts: a thread joins 8 dims of its rows
         const bool few = parts.n <= 8;
         for (int row = r16; few && row < T << a.group_shift; row += kW * 4) {
           Joined j;

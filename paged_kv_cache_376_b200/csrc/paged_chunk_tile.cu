@@ -776,7 +776,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const float2 v = scaled(z, e);
                 // the special function unit is the floor of this loop: every
                 // fourth pair goes through the FMA units
-                const float2 w = (e & 3) == 3
+                const float2 w = (e & 3) == 0
                                      ? exp2_cubic(v)
                                      : make_float2(fast_exp2(v.x),
                                                    fast_exp2(v.y));
