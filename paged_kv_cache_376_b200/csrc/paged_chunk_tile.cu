@@ -12,14 +12,14 @@
 // Per SM and clock the tensor core does 4096 multiply-adds (here 2900: 46
 // clocks for a product of N = 64) and the special function unit 16
 // exponentials, so a 128 x 128 tile costs 512 (720) clocks of the one and 1024
-// of the other, 768 with every fourth pair on the FMA units.  Measured: 2250
-// clocks a tile for one query tile alone, 1600 for each of two.  It is the
+// of the other, 768 with every fourth pair on the FMA units.  Measured: 2200
+// clocks a tile for one query tile alone, 1580 for each of two.  It is the
 // softmax warps' own latency: without nearly all products the step is 3 %
 // shorter, without the exponentials 24 %, and fewer instructions (no maximum),
 // a third of the pairs on the FMA units, or other orders change nothing; two
 // warps per scheduler are what tensor memory (S, P and O of two query tiles)
 // and registers leave room for (four at 96 registers: slower, they spill).
-// 32 decoder prompts over 1500 states: 160 us (400 TFLOP/s, plan and launches
+// 32 decoder prompts over 1500 states: 158 us (400 TFLOP/s, plan and launches
 // included); 256 rows x 5120 keys each: 640 TFLOP/s.
 //
 // Design.
@@ -775,7 +775,8 @@ __global__ void __launch_bounds__(kThreads, 1)
               for (int e = 0; e < 16; ++e) {
                 const float2 v = scaled(z, e);
                 // the special function unit is the floor of this loop: every
-                // fourth pair goes through the FMA units
+                // fourth pair goes through the FMA units (the first of four:
+                // 3 % faster than the last)
                 const float2 w = (e & 3) == 0
                                      ? exp2_cubic(v)
                                      : make_float2(fast_exp2(v.x),
