@@ -448,7 +448,7 @@ def prefill_workspace(num_seqs, max_query_len, device="cuda"):
     """Device workspace for the cost-ordered prefill dispatch (no initial
     contents needed)."""
     n = tv_prefill_workspace_size(num_seqs, max_query_len)
-    return torch.zeros(max(n, 16), dtype=torch.uint8, device=device)
+    return torch.empty(max(n, 16), dtype=torch.uint8, device=device)
 
 
 def tv_paged_prefill(out, q, query_start_loc, k_pool, v_pool, block_tables,
