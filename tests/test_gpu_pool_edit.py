@@ -224,5 +224,41 @@ def test_captured_compaction_replays_on_new_contents():
         p.check()
 
 
+def test_captured_page_copies_follow_one_another():
+    """A copy behind a memcpy, a copy that reads what the last one wrote, and a
+    further layer's copy behind a compaction, in one graph."""
+    n = 120
+    bt, ctx = U.random_pool(12, n, 12, 16)
+    p = Pair(n, bt, ctx, 16)
+    moves, count = _lib.pool_moves(n)
+    k2, v2 = p.g_kp.clone(), p.g_vp.clone()
+    kp = np.random.default_rng(2).integers(
+        0, 1 << 16, (n, 16, 2, 64)).astype(np.uint16)
+    fresh = bf16_tensor(kp)
+    gk, gv = torch.empty_like(fresh), torch.empty_like(fresh)
+    a, b, c = (i32_tensor(np.arange(i, i + 40)) for i in (0, 40, 80))
+    st = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g, stream=st):
+        gv.copy_(fresh)
+        gk.copy_(fresh)
+        _lib.tv_page_copy(gk, gv, a, b, err=p.err)
+        _lib.tv_page_copy(gk, gv, b, c, err=p.err)
+        _lib.tv_pool_compact(p.state, p.g_bt, p.g_ctx, moves, count, p.g_kp,
+                             p.g_vp, err=p.err)
+        _lib.tv_page_copy(k2, v2, moves[0], moves[1], num_pairs=count,
+                          err=p.err)
+    p.pool.compact(p.bt, p.ctx, p.kp, p.vp)
+    want = np.concatenate([kp[:40]] * 3)
+    for _ in range(3):              # the second compaction finds nothing to move
+        g.replay()
+        np.testing.assert_array_equal(bf16_bits(gk), want)
+        np.testing.assert_array_equal(bf16_bits(gv), want)
+        np.testing.assert_array_equal(bf16_bits(k2), bf16_bits(p.g_kp))
+        np.testing.assert_array_equal(bf16_bits(v2), bf16_bits(p.g_vp))
+        p.check()
+
+
 def test_pages_for_is_the_kernels_rounding():
     assert [pages_for(n, 16) for n in (0, 1, 16, 17)] == [0, 1, 1, 2]
