@@ -415,7 +415,9 @@ tv_status tv_prefill_workspace_size(int num_seqs, int max_query_len,
  *                    tv_chunk_workspace_size() bytes, 16-byte aligned, zeroed
  *                    once before its first use (every call leaves its
  *                    counters at zero again, except one that flagged
- *                    TV_DEVERR_TIMEOUT).  Calls that overlap on the GPU need
+ *                    TV_DEVERR_TIMEOUT).  One buffer serves calls of this and
+ *                    of tv_paged_cross_attention of every shape whose size it
+ *                    has, in any order.  Calls that overlap on the GPU need
  *                    separate workspaces.
  *   workspace_bytes  its size; too small returns TV_ERR_INVALID_ARG
  * A sequence with T_s > C, T_s > max_query_len or rows outside q is flagged

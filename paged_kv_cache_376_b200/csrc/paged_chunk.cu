@@ -595,8 +595,8 @@ __global__ void __launch_bounds__(kThreads, 3)
 // end of a sequence moves there, so short sequences are never cut.
 //
 // A sequence inside one range is written directly.  One that is cut leaves a
-// part (m, l, unscaled output) per range in the workspace and counts up its
-// counter; the CTA that completes the count joins the parts, in the order of
+// part (m, l, unscaled output) per range in the workspace and counts up the
+// counter of the first boundary inside it; the CTA that completes the count joins the parts, in the order of
 // the ranges (results do not depend on timing), and sets the counter back to
 // zero.  No CTA waits for another.
 //
@@ -882,11 +882,19 @@ __global__ void __launch_bounds__((compute_warps(MB) + 1) * 32,
     struct Parts {
       int g0, n;
     };
-    auto parts_of = [&](int s) {      // groups with a boundary inside it
-      const int z0 = sm.pre[s] + kSnap, z1 = sm.pre[s + 1] - kSnap;
-      const int g0 = (int)(((int64_t)z0 * NG + W - 1) / W);
+    auto first_inside = [&](int s) {  // first group with a boundary inside it
+      return (int)(((int64_t)(sm.pre[s] + kSnap) * NG + W - 1) / W);
+    };
+    auto parts_of = [&](int s) {
+      const int z1 = sm.pre[s + 1] - kSnap;
+      const int g0 = first_inside(s);
       const int g1 = (int)(((int64_t)(z1 + 1) * NG + W - 1) / W) - 1;
       return Parts{g0, g1 - g0 + 2};
+    };
+    // A boundary lies inside one sequence, so its group's word is that
+    // sequence's own, and there is one per CTA for any batch.
+    auto counter_of = [&](int s) {
+      return a.ws_counters + first_inside(s) * Hkv + head;
     };
     const int r16 = threadIdx.x >> 3, k8 = threadIdx.x & 7;
     int cut_seq[2] = {-1, -1};        // the cut sequences of the range's ends
@@ -965,8 +973,7 @@ __global__ void __launch_bounds__((compute_warps(MB) + 1) * 32,
         compute_barrier<kW>();
         if (threadIdx.x == 0) {
           __threadfence();   // the CTA's part, ordered by the barrier
-          counted[slot] =
-              atomicAdd(a.ws_counters + (size_t)seq * Hkv + head, 1);
+          counted[slot] = atomicAdd(counter_of(seq), 1);
         }
       }
       p0 = end;
@@ -1062,7 +1069,7 @@ __global__ void __launch_bounds__((compute_warps(MB) + 1) * 32,
                 .write(out_row(a, qs, head, row0 + r16), k8);
           compute_barrier<kW>();
         }
-        if (threadIdx.x == 0) a.ws_counters[(size_t)s * Hkv + head] = 0;
+        if (threadIdx.x == 0) *counter_of(s) = 0;
       }
     }
     if (failed && lane == 0) flag_error(a.err, DEVERR_TIMEOUT);

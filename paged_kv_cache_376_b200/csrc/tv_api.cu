@@ -808,8 +808,10 @@ tv_status tv_paged_prefill(void* out, const void* q, int64_t num_query_rows,
 
 // ---- attention of a chunk of rows per sequence -----------------------------------
 
-// Workspace: the counters (zero between calls) of sequences and blocks that are
-// cut along their keys, then their parts and the tile kernel's plan.
+// Workspace: the counters (zero between calls) of the sequences that are cut along
+// their keys, then their parts and the tile kernel's plan.  The counters have one
+// place and size on a device whatever the call's shape, one word per CTA of the
+// balanced grid, so that no call's parts lie where another's counters are.
 static int chunk_ctas() { return device_sms() * tv::kChunkCtasPerSm; }
 
 struct ChunkWorkspace {
@@ -817,13 +819,13 @@ struct ChunkWorkspace {
 };
 
 static ChunkWorkspace chunk_workspace(int num_seqs, int max_query_len,
-                                      int num_kv_heads, int group_shift) {
+                                      int group_shift) {
   auto up = [](size_t n) { return (n + 255) / 256 * 256; };
   const size_t sms = device_sms();
   const bool tiles =
       ((int64_t)max_query_len << group_shift) > tv::kChunkPartRows;
   ChunkWorkspace w;
-  w.parts = counters_bytes(num_seqs, num_kv_heads);
+  w.parts = up((size_t)chunk_ctas() * sizeof(int32_t));
   w.plan = w.parts + up((size_t)chunk_ctas() * 2 * tv::kChunkPartFloats *
                         sizeof(float));
   w.joins = w.plan + (tiles ? 256 : 0);
@@ -851,7 +853,7 @@ tv_status tv_chunk_workspace_size(int num_seqs, int max_query_len,
   if (((int64_t)max_query_len << shift) > 65535ll * 16)
     return TV_ERR_UNSUPPORTED;
   if (device_sms() <= 0) return cuda_status(cudaErrorUnknown);
-  *bytes = chunk_workspace(num_seqs, max_query_len, num_kv_heads, shift).bytes;
+  *bytes = chunk_workspace(num_seqs, max_query_len, shift).bytes;
   return TV_OK;
 }
 
@@ -894,7 +896,7 @@ static tv_status chunk_common(void* out, const void* q, int64_t num_query_rows,
   const int shift = group_shift_of(group);
   ChunkWorkspace ws{};
   if (workspace) {
-    ws = chunk_workspace(num_seqs, max_query_len, num_kv_heads, shift);
+    ws = chunk_workspace(num_seqs, max_query_len, shift);
     if (!aligned16(workspace) || workspace_bytes < ws.bytes)
       return TV_ERR_INVALID_ARG;
   }

@@ -281,7 +281,7 @@ struct ChunkArgs {
   // block and sequence), which serves the sequences of up to stream_rows rows.
   int balanced_ctas;             // kChunkCtasPerSm per SM
   int stream_rows;
-  int32_t* ws_counters;          // [B][Hkv], zero between calls
+  int32_t* ws_counters;          // [balanced_ctas], zero between calls
   float* ws_parts;               // [balanced_ctas][2][kChunkPartFloats]
   // The tile kernel's part of the workspace (tile_ctas 0: not launched).
   int tile_ctas;
