@@ -273,9 +273,11 @@ tv_status tv_decode_workspace_size(int num_seqs, int num_q_heads,
  * CTA slots, and the tail that mixed context lengths cause.
  *   workspace        device memory of at least tv_decode_workspace_size()
  *                    bytes, 16-byte aligned, ZERO-FILLED before its first
- *                    use; each call leaves it zero-filled again unless a
- *                    bounded wait ran out (TV_DEVERR_TIMEOUT), after which
- *                    it must be zero-filled again
+ *                    use; each call leaves its counters at zero again unless
+ *                    a bounded wait ran out (TV_DEVERR_TIMEOUT), after which
+ *                    it must be zero-filled again.  One buffer serves batches
+ *                    of every shape whose size it has, in any order (it is
+ *                    not that of tv_paged_chunk)
  *   workspace_bytes  its size; too small returns TV_ERR_INVALID_ARG
  *   other arguments as tv_paged_decode / tv_paged_decode_append.
  * Calls that overlap on the GPU (unordered streams) need separate

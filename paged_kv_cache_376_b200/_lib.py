@@ -608,7 +608,8 @@ def tv_decode_workspace_size(num_seqs, num_q_heads, num_kv_heads,
 
 def decode_workspace(num_seqs, num_q_heads, num_kv_heads, device=None):
     """A zero-filled uint8 workspace of the size tv_decode_workspace_size
-    gives (the balanced decode leaves it zero-filled after every call)."""
+    gives (the balanced decode leaves its counters at zero after every
+    call)."""
     n = tv_decode_workspace_size(num_seqs, num_q_heads, num_kv_heads)
     return torch.zeros(n, dtype=torch.uint8, device=device or "cuda")
 

@@ -41,10 +41,12 @@
 //    item cut by range boundaries is a set of segments, one per group; each
 //    writes (m, l, acc) for its G heads to its workspace slot (slot 0 for
 //    the first segment of its range, 1 for the last), fences, and
-//    increments the item's counter; the warp that brings the counter to the
-//    number of segments merges them with the log-sum-exp rule of the
-//    split-KV merge and resets the counter to zero.  Nothing ever waits on
-//    another warp, so no spin-wait exists beyond the bounded TMA waits.
+//    increments the item's counter (the word of the warp that holds its first
+//    page, so that batches of every shape count in the same words); the warp
+//    that brings the counter to the number of segments merges them with the
+//    log-sum-exp rule of the split-KV merge and resets the counter to zero.
+//    Nothing ever waits on another warp, so no spin-wait exists beyond the
+//    bounded TMA waits.
 //  * Fused append: the page holding position ctx-1 is loaded with the new K
 //    and V rows of its KV head (two 128-byte bulk copies into a side slot of
 //    the same ring stage, same mbarrier); the warp copies them over the
@@ -477,7 +479,6 @@ __global__ void __launch_bounds__(kThreads, G <= 4 ? 4 : 2)
         L0 += __shfl_xor_sync(0xffffffffu, L0, off);
         L1 += __shfl_xor_sync(0xffffffffu, L1, off);
       }
-      const int u = seq * Hkv + head;
       __nv_bfloat16* out_item =
           a.out + ((size_t)seq * a.num_q_heads + head * G) * kD;
       if (seg_at_item_start && last_of_item) {
@@ -528,14 +529,17 @@ __global__ void __launch_bounds__(kThreads, G <= 4 ? 4 : 2)
         }
         __threadfence();
         __syncwarp();
-        int old = 0;
-        if (lane == 0) old = atomicAdd(a.ws_counters + u, 1);
-        old = __shfl_sync(0xffffffffu, old, 0);
         const int item_x = sm.pre[seq];     // first page of sequence seq
-        const int g_first = owner(item_x);
+        const int g_first = seg_at_item_start ? grp_id : owner(item_x);
+        // the word of the warp that holds the item's first page: one cut item
+        // crosses the end of its range
+        int32_t* counter = a.ws_counters + g_first * Hkv + head;
+        int old = 0;
+        if (lane == 0) old = atomicAdd(counter, 1);
         int g_last = grp_id;                // this group holds the last page
         if (!last_of_item)
           g_last = owner(item_x + sm.pre[seq + 1] - sm.pre[seq] - 1);
+        old = __shfl_sync(0xffffffffu, old, 0);
         if (old == g_last - g_first) {
           // every other segment is in memory: merge them all.  Segment k
           // (k = 0 .. nseg-1) is in warp head of group g_first + k, slot 0
@@ -653,7 +657,7 @@ __global__ void __launch_bounds__(kThreads, G <= 4 ? 4 : 2)
               *reinterpret_cast<uint4*>(out_item + h * kD + chk * 8) = o;
             }
           }
-          if (lane == 0) a.ws_counters[u] = 0;
+          if (lane == 0) *counter = 0;
         }
       }
     }

@@ -258,8 +258,9 @@ tv_status tv_kv_append_mrope(void* q_out, const void* q, int64_t q_stride,
       tv::launch_kv_append_mrope(a, static_cast<cudaStream_t>(stream)));
 }
 
-// Device workspace of the work-balanced decode: per-item counters, then two
-// partial-result slots per warp of the persistent grid.
+// Device workspace of the work-balanced decode: the counters of cut items, a word
+// per warp of the grid (an SM holds at most 64), in one place for calls of every
+// shape; then two partial-result slots per warp.
 struct BalancedWorkspace {
   void* base;
   size_t bytes;
@@ -267,8 +268,8 @@ struct BalancedWorkspace {
 
 static int device_sms() { return tv::device_sm_count(); }
 
-static size_t counters_bytes(int num_seqs, int num_kv_heads) {
-  return ((size_t)num_seqs * num_kv_heads * 4 + 255) / 256 * 256;
+static size_t counters_bytes() {
+  return (size_t)device_sms() * 64 * sizeof(int32_t);
 }
 
 static int balanced_ctas(int group) {
@@ -370,7 +371,7 @@ static tv_status decode_common(void* out, float* partial_out,
   if (balanced) {
     const int cap = balanced_ctas(group);
     if (cap <= 0) return cuda_status(cudaErrorUnknown);
-    const size_t cb = counters_bytes(num_seqs, num_kv_heads);
+    const size_t cb = counters_bytes();
     if (ws->bytes < cb + partials_bytes(cap)) return TV_ERR_INVALID_ARG;
     // groups of num_kv_heads warps, each with >= kMinPagesPerWarp pages
     // (num_seqs * max_blocks_per_seq bounds the page count from above)
@@ -448,7 +449,7 @@ tv_status tv_decode_workspace_size(int num_seqs, int num_q_heads,
   if (num_seqs < 0) return TV_ERR_INVALID_ARG;
   const int cap = balanced_ctas(num_q_heads / num_kv_heads);
   if (cap <= 0) return cuda_status(cudaErrorUnknown);
-  *bytes = counters_bytes(num_seqs, num_kv_heads) + partials_bytes(cap);
+  *bytes = counters_bytes() + partials_bytes(cap);
   return TV_OK;
 }
 

@@ -100,7 +100,7 @@ struct DecodeArgs {
   // work-balanced decode only
   int num_seqs;
   int num_kv_heads;
-  int32_t* ws_counters;          // [B * Hkv], zero between launches
+  int32_t* ws_counters;          // [warps of the grid], zero between launches
   float* ws_partials;            // [warps][2][kSlotFloats]
 };
 
