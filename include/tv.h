@@ -426,8 +426,9 @@ tv_status tv_prefill_workspace_size(int num_seqs, int max_query_len,
  * TV_DEVERR_BAD_QUERY and skipped.  scale must be positive
  * (TV_ERR_INVALID_ARG otherwise, as tv_paged_prefill); max_query_len times the
  * group size is at most 2^20 - 16.  Scores, weights, their sum and the output's
- * sum are fp32; the weights enter the product with V in bf16, with 16 bits for
- * rows of a block whose first row sees fewer than 512 keys.  With a workspace,
+ * sum are fp32; the weights enter the product with V as two bf16 terms (16
+ * bits), as in tv_paged_prefill.  A row's bits do not depend on what the other
+ * rows of the call hold.  With a workspace,
  * up to 1024 sequences (and max_blocks_per_seq * page_size * num_seqs / 16 up
  * to 2^31 - 1) are split over keys, and sequences of more than 32 rows x heads
  * per KV head run on the tcgen05 tensor cores.  A key of a bad page is left

@@ -26,10 +26,10 @@
 // instead).  Two kernels share this step: one CTA per (KV head, block of rows,
 // sequence), for calls without a workspace, and a balanced grid.
 //
-// P enters the second product in bf16.  A weight's rounding (up to 2^-8)
-// averages out over the keys of a row, except where there are few: blocks
-// whose first row sees fewer than kChunkExactKeys keys add P's remainder,
-// P - bf16(P), with a second product, as the decode and the prefill always do.
+// P enters the second product with 16 bits, as in the decode and the prefill:
+// bf16(P), and the remainder P - bf16(P) in a second product over the same V
+// fragments (a weight is then off by at most 2^-16; bf16(P) alone would be by
+// 2^-8, which shows where few keys carry a row).
 #include "tv_chunk.cuh"
 #include "tv_decode.cuh"
 
@@ -45,7 +45,6 @@ constexpr int kRowBytes = kD * 2;
 constexpr int kSliceBytes = kPS * kRowBytes;
 constexpr int kStageBytes = 2 * kSliceBytes;
 constexpr float kLazy = 8.f;     // log2 of the growth the running sums allow
-constexpr int kExactKeys = kChunkExactKeys;
 
 template <int kW>
 struct ChunkRing {
@@ -171,7 +170,6 @@ struct WarpRows {
                                        const uint32_t (&voff)[4], float sl,
                                        int lane) {
     const int c = lane & 3;
-    const bool exact = w.first_limit + 1 < kExactKeys;
     uint8_t* vbase = kbase + kSliceBytes;
     // warp-uniform: every row sees every token of the page
     const bool full_page = page_ok && tok0 + kPS - 1 <= w.first_limit;
@@ -215,10 +213,18 @@ struct WarpRows {
     //      tokens, the row's maximum is taken, its offset moved and the
     //      weights are done again; the check is off the path to the
     //      exponentials, and needs no exchange between lanes -----------------
-    uint32_t ph[MB][4];
+    uint32_t ph[MB][4], pl[MB][4];    // and the weights' remainders
     auto weight = [&](int b, int n, int e, int k) {
       const float mu = m[b][e] == -INFINITY ? 0.f : m[b][e];
       return fast_exp2(fmaf(s[b][n][2 * e + k], sl, -mu));
+    };
+    auto split = [&](int b, int i, float p0, float p1) {
+      const uint32_t h = pack_bf16x2(p0, p1);
+      ph[b][i] = h;
+      const float2 rest =
+          __ffma2_rn(make_float2(bf16_lo(h), bf16_hi(h)),
+                     make_float2(-1.f, -1.f), make_float2(p0, p1));
+      pl[b][i] = pack_bf16x2(rest.x, rest.y);
     };
     float top = -INFINITY, ls[MB][2];
 #pragma unroll
@@ -234,7 +240,7 @@ struct WarpRows {
           top = fmax3(top, x0, x1);
           const float p0 = fast_exp2(x0), p1 = fast_exp2(x1);
           ls[b][e] += p0 + p1;
-          ph[b][2 * n + e] = pack_bf16x2(p0, p1);
+          split(b, 2 * n + e, p0, p1);
         }
       }
     if (!full_page || __any_sync(0xffffffffu, top > kLazy)) {
@@ -272,7 +278,7 @@ struct WarpRows {
           for (int n = 0; n < 2; ++n) {
             const float p0 = weight(b, n, e, 0), p1 = weight(b, n, e, 1);
             ls[b][e] += p0 + p1;
-            ph[b][2 * n + e] = pack_bf16x2(p0, p1);
+            split(b, 2 * n + e, p0, p1);
           }
         }
     }
@@ -291,28 +297,8 @@ struct WarpRows {
       for (int b = 0; b < MB; ++b) {
         mma_bf16_16816(acc[b][2 * t], ph[b], vf[0], vf[1]);
         mma_bf16_16816(acc[b][2 * t + 1], ph[b], vf[2], vf[3]);
-      }
-    }
-    if (exact) {   // the weights' remainders
-#pragma unroll
-      for (int b = 0; b < MB; ++b)
-#pragma unroll
-        for (int e = 0; e < 2; ++e)
-#pragma unroll
-          for (int n = 0; n < 2; ++n) {
-            const uint32_t h = ph[b][2 * n + e];
-            ph[b][2 * n + e] = pack_bf16x2(weight(b, n, e, 0) - bf16_lo(h),
-                                           weight(b, n, e, 1) - bf16_hi(h));
-          }
-#pragma unroll
-      for (int t = 0; t < 4; ++t) {
-        uint32_t vf[4];
-        ldsm_x4_trans(vb + voff[t], vf);
-#pragma unroll
-        for (int b = 0; b < MB; ++b) {
-          mma_bf16_16816(acc[b][2 * t], ph[b], vf[0], vf[1]);
-          mma_bf16_16816(acc[b][2 * t + 1], ph[b], vf[2], vf[3]);
-        }
+        mma_bf16_16816(acc[b][2 * t], pl[b], vf[0], vf[1]);
+        mma_bf16_16816(acc[b][2 * t + 1], pl[b], vf[2], vf[3]);
       }
     }
     return !full_page;

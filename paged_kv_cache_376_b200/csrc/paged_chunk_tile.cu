@@ -11,16 +11,15 @@
 // What bounds it: 2 x 64 multiply-adds and one exponential per (row, key).
 // Per SM and clock the tensor core does 4096 multiply-adds (here 2900: 46
 // clocks for a product of N = 64) and the special function unit 16
-// exponentials, so a 128 x 128 tile costs 512 (720) clocks of the one and 1024
-// of the other, 768 with every fourth pair on the FMA units.  Measured: 2200
-// clocks a tile for one query tile alone, 1580 for each of two.  It is the
-// softmax warps' own latency: without nearly all products the step is 3 %
-// shorter, without the exponentials 24 %, and fewer instructions (no maximum),
-// a third of the pairs on the FMA units, or other orders change nothing; two
-// warps per scheduler are what tensor memory (S, P and O of two query tiles)
-// and registers leave room for (four at 96 registers: slower, they spill).
-// 32 decoder prompts over 1500 states: 158 us (400 TFLOP/s, plan and launches
-// included); 256 rows x 5120 keys each: 640 TFLOP/s.
+// exponentials, so a 128 x 128 tile costs 768 (1080) clocks of the one, P V
+// counted twice for P's two terms, and 1024 of the other.  What it takes longer
+// is the softmax warps' own latency: two warps per scheduler are what tensor
+// memory (S, P and O of two query tiles) and registers leave room for (four at
+// 96 registers: slower, they spill).  32 decoder prompts over 1500 states: 188
+// us (339 TFLOP/s, plan and launches included), 162 with P in bf16 alone.  Every
+// fourth pair of exponentials as a polynomial on the FMA units gains 1 % beside
+// P's two terms (187.3 against 185.3 us) and was left out: a row's bits would
+// depend on which way its neighbours' offsets send the warp.
 //
 // Design.
 //  * A plan kernel (one CTA) lists the work: (sequence, block of 256 rows),
@@ -42,11 +41,11 @@
 //  * The softmax exponentiates against its offset as it stands and takes the
 //    maximum beside it; only where a row's maximum grew by more than 2^8 (and
 //    at a unit's first half) does it move the offset, rescale O and the sum
-//    and exponentiate again from the registers.
-//  * P enters the second product in bf16.  A weight's rounding (up to 2^-8)
-//    averages out over the keys of a row, except where there are few: units
-//    whose first row sees fewer than kExactKeys keys add P's remainder,
-//    P - bf16(P), in a second pass over the tile.
+//    and exponentiate again.  A row's offset depends on its own scores alone,
+//    and so do its bits.
+//  * P enters the second product with 16 bits: bf16(P), and the remainder
+//    P - bf16(P) in a second pass over the tile (a weight is off by at most
+//    2^-16 from it, as in the prefill).
 //  * What a row does not see never reaches it: on the tiles that cross the
 //    diagonal or the end, warp 0 zeroes the V rows behind the last key and
 //    takes infinities and NaNs out of V; it notes per dim the first key
@@ -78,7 +77,6 @@ constexpr int kSCol = 0;                  // S, then P, in buffer b of query
                                           // tile t: [64 (3 t + b), +64)
 constexpr int kOCol = 384;                // O of tile t: [384 + 64 t, +64)
 constexpr float kLazy = 8.f;              // log2 of the growth allowed
-constexpr int kExactKeys = kChunkExactKeys;   // see the file comment
 constexpr int kMinTiles = 8;              // key tiles worth a unit of their own
 
 constexpr uint32_t kIdescQK = idesc_bf16_f32(kBM, kHalf, false);
@@ -335,6 +333,28 @@ __device__ __forceinline__ void tmem_wait32(uint32_t (&r)[32]) {
                : "memory");
 }
 
+// Stores without their wait: a thread's 32 registers, or the first 16 of 32.
+#define TV_IN8(r, i)                                                    \
+  "r"(r[i]), "r"(r[i + 1]), "r"(r[i + 2]), "r"(r[i + 3]), "r"(r[i + 4]), \
+      "r"(r[i + 5]), "r"(r[i + 6]), "r"(r[i + 7])
+__device__ __forceinline__ void tmem_put32(uint32_t taddr,
+                                           const uint32_t (&r)[32]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1, %2, %3, %4, %5, %6, "
+      "%7, %8, %9, %10, %11, %12, %13, %14, %15, %16, %17, %18, %19, %20, %21, "
+      "%22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};" ::"r"(taddr),
+      TV_IN8(r, 0), TV_IN8(r, 8), TV_IN8(r, 16), TV_IN8(r, 24)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_put16(uint32_t taddr,
+                                           const uint32_t (&r)[32]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, "
+      "%7, %8, %9, %10, %11, %12, %13, %14, %15, %16};" ::"r"(taddr),
+      TV_IN8(r, 0), TV_IN8(r, 8)
+      : "memory");
+}
+
 __device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
   asm volatile(
       "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
@@ -354,32 +374,6 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr,
       "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]),
       "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
       : "memory");
-}
-
-// 2^x of a pair on the FMA units: x = n + f, |f| <= 1/2 (n by adding and
-// subtracting 1.5 x 2^23), 2^f by the cubic of least relative error on that
-// range (Remez exchange; 7.5e-5, against the up to 3.9e-3 of the bf16 that it becomes),
-// 2^n from its exponent bits.  Below 2^-126 it stays there.
-__device__ __forceinline__ float max_nan(float a, float b) {
-  float r;
-  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
-  return r;
-}
-__device__ __forceinline__ float2 exp2_cubic(float2 x) {
-  const float2 big = make_float2(12582912.f, 12582912.f);
-  const float2 nbig = make_float2(-12582912.f, -12582912.f);
-  x = make_float2(max_nan(x.x, -126.f), max_nan(x.y, -126.f));
-  const float2 t = __fadd2_rn(x, big);
-  const float2 n = __fadd2_rn(t, nbig);
-  const float2 f = __ffma2_rn(n, make_float2(-1.f, -1.f), x);
-  float2 p = __ffma2_rn(make_float2(0.0551716685f, 0.0551716685f), f,
-                        make_float2(0.242611125f, 0.242611125f));
-  p = __ffma2_rn(p, f, make_float2(0.693260968f, 0.693260968f));
-  p = __ffma2_rn(p, f, make_float2(0.999928057f, 0.999928057f));
-  const float2 scale =
-      make_float2(__int_as_float((__float_as_int(t.x) << 23) + 0x3f800000),
-                  __int_as_float((__float_as_int(t.y) << 23) + 0x3f800000));
-  return __fmul2_rn(p, scale);   // NaN x stays NaN
 }
 
 // Rows [r0, 128) of a V tile that holds the keys key0 .. : rows behind the last
@@ -636,7 +630,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         Turn& h = turn[0];
         const int n = u.n[t];
         const int edge = u.edge0 - u.e.tile0;
-        const int parts = u.b.first_limit + 1 < kExactKeys ? 2 : 1;
         if (n > 0 && results > 0)   // the last unit's O has been read
           ok = wait_warp(&sm.o_free[t], (results - 1) & 1);
         for (int j = 0; ok && j < n_tiles; ++j, ++it) {
@@ -671,9 +664,8 @@ __global__ void __launch_bounds__(kThreads, 1)
               const uint32_t v_half = v_lo + half * (kHalf * kRowBytes >> 4);
               issue_pv(tmem + kOCol + t * kD, p_col, v_half, hi_v,
                        (j | half) != 0);
-              if (parts == 2)
-                issue_pv(tmem + kOCol + t * kD, p_col + kHalf / 2, v_half,
-                         hi_v, true);
+              issue_pv(tmem + kOCol + t * kD, p_col + kHalf / 2, v_half, hi_v,
+                       true);   // the remainder
               tc_commit(smem_u32(&sm.o_done[t][h.b]));
             }
             __syncwarp();
@@ -732,17 +724,17 @@ __global__ void __launch_bounds__(kThreads, 1)
                             ? first_limit + (real ? t * per + qi : tb - 1)
                             : u.b.key_end - 1;
       const int tile_limit = kCausal ? first_limit + t * per : limit;
-      const bool exact = first_limit + 1 < kExactKeys;
       float m_run = -INFINITY, l_run = 0.f;
       // ---- the halves: two loads of 32 columns, the second in flight while the
       //      first is exponentiated against the offset m_run as it stands, the
       //      maximum beside it.  Halves with hidden keys, the first of a unit
       //      and those where a row's maximum grew by 2^8 take the maximum
-      //      first, move the offset (rescaling O and the sum) and
-      //      exponentiate from the registers (again).  The loop's scalar code
-      //      is kept short: it costs as much time as the exponentials ------------
+      //      first, move the offset (rescaling O and the sum) and exponentiate
+      //      (again, from tensor memory: the first weights' remainders have
+      //      taken the scores' registers).  The loop's scalar code is kept
+      //      short: it costs as much time as the exponentials --------------------
       const int halves = ok ? n : 0;
-      const int plain = exact ? 0 : (tile_limit + 1 - tile0 * kBN) / kHalf;
+      const int plain = (tile_limit + 1 - tile0 * kBN) / kHalf;
       volatile const int32_t* bad_unit = &sm.bad_unit[ub];
 #pragma unroll 1
       for (int i = 0; i < halves; ++i) {
@@ -769,21 +761,25 @@ __global__ void __launch_bounds__(kThreads, 1)
             mx[e & 1] = fmax3(mx[e & 1], __uint_as_float(z[2 * e]),
                               __uint_as_float(z[2 * e + 1]));
           };
-          if (__builtin_expect(!again, 1)) {
-            auto quick = [&](const uint32_t (&z)[32], int base) {
+          // a pair's weights in two bf16 terms, the remainder in place of the
+          // scores
+          auto split = [&](float2 w, int e, uint32_t& z) {
+            hi[e] = pack_bf16x2(w.x, w.y);
+            const float2 rest =
+                __ffma2_rn(make_float2(bf16_lo(hi[e]), bf16_hi(hi[e])),
+                           make_float2(-1.f, -1.f), w);
+            z = pack_bf16x2(rest.x, rest.y);
+          };
+          const bool quick_half = !again;
+          if (__builtin_expect(quick_half, 1)) {
+            auto quick = [&](uint32_t (&z)[32], int base) {
 #pragma unroll
               for (int e = 0; e < 16; ++e) {
                 const float2 v = scaled(z, e);
-                // the special function unit is the floor of this loop: every
-                // fourth pair goes through the FMA units (the first of four:
-                // 3 % faster than the last)
-                const float2 w = (e & 3) == 0
-                                     ? exp2_cubic(v)
-                                     : make_float2(fast_exp2(v.x),
-                                                   fast_exp2(v.y));
+                const float2 w = make_float2(fast_exp2(v.x), fast_exp2(v.y));
                 maximum(z, e);
                 sum = __fadd2_rn(sum, w);
-                hi[base + e] = pack_bf16x2(w.x, w.y);
+                split(w, base + e, z[e]);
               }
             };
             quick(x, 0);
@@ -833,6 +829,12 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
           }
           if (__builtin_expect(again, 0)) {
+            if (quick_half) {   // the scores have given way to remainders
+              tmem_ld32(buf, x);
+              tmem_ld32(buf + 32, y);
+              tmem_wait32(x);
+              tmem_wait32(y);
+            }
             m_use = m_run == -INFINITY ? 0.f : m_run;
             sum = make_float2(0.f, 0.f);
 #pragma unroll
@@ -840,23 +842,15 @@ __global__ void __launch_bounds__(kThreads, 1)
               const float2 v = e < 16 ? scaled(x, e) : scaled(y, e - 16);
               const float2 w = make_float2(fast_exp2(v.x), fast_exp2(v.y));
               sum = __fadd2_rn(sum, w);
-              hi[e] = pack_bf16x2(w.x, w.y);
-              if (exact) {   // P's remainder, in the place of the scores
-                const uint32_t lo = pack_bf16x2(w.x - bf16_lo(hi[e]),
-                                                w.y - bf16_hi(hi[e]));
-                if (e < 16) x[e] = lo;
-                else y[e - 16] = lo;
-              }
+              split(w, e, e < 16 ? x[e] : y[e - 16]);
             }
           }
           l_run += sum.x + sum.y;
           // P takes the place of S (the remainder behind it)
-          tmem_st32(buf, hi);
-          if (__builtin_expect(exact, 0)) {
-#pragma unroll
-            for (int e = 0; e < 32; ++e) hi[e] = e < 16 ? x[e] : y[e - 16];
-            tmem_st32(buf + 32, hi);
-          }
+          tmem_put32(buf, hi);
+          tmem_put16(buf + 32, x);
+          tmem_put16(buf + 48, y);
+          asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
           tc_fence_before();
           __syncwarp();
           if (lane == 0) mbar_arrive(smem_u32(&sm.p_full[t][h.b]));

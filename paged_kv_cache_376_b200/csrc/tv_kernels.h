@@ -296,8 +296,6 @@ constexpr int kChunkPartRows = 32;      // rows x heads per KV head
 // m, l and the unscaled output of one part
 constexpr int kChunkPartFloats = kChunkPartRows * (2 + 64);
 constexpr int kChunkCtasPerSm = 3;     // at most
-// below so many visible keys P keeps 16 bits in P V, from there on 8
-constexpr int kChunkExactKeys = 512;
 // m, l and the unscaled output of two query tiles of 128 rows
 constexpr int kTilePartFloats = 2 * 128 * (2 + 64);
 __host__ __device__ inline int chunk_tile_blocks(int max_query_len,
