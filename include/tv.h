@@ -432,8 +432,8 @@ tv_status tv_prefill_workspace_size(int num_seqs, int max_query_len,
  * up to 1024 sequences (and max_blocks_per_seq * page_size * num_seqs / 16 up
  * to 2^31 - 1) are split over keys, and sequences of more than 32 rows x heads
  * per KV head run on the tcgen05 tensor cores.  A key of a bad page is left
- * out; a row
- * that sees no key comes out zero.  What a key that a row does not see holds,
+ * out; a row that sees no key, or whose every score is minus infinity, comes
+ * out zero.  What a key that a row does not see holds,
  * NaN and infinities too, does not reach that row; an infinity or NaN in V
  * that it sees makes that element of its output non-finite.
  */

@@ -128,7 +128,7 @@ struct WarpRows {
   __device__ __forceinline__ void clear() {
 #pragma unroll
     for (int b = 0; b < MB; ++b) {
-      m[b][0] = m[b][1] = -INFINITY;
+      m[b][0] = m[b][1] = kNoOffset;
       l[b][0] = l[b][1] = 0.f;
 #pragma unroll
       for (int n = 0; n < 8; ++n)
@@ -215,8 +215,7 @@ struct WarpRows {
     //      exponentials, and needs no exchange between lanes -----------------
     uint32_t ph[MB][4], pl[MB][4];    // and the weights' remainders
     auto weight = [&](int b, int n, int e, int k) {
-      const float mu = m[b][e] == -INFINITY ? 0.f : m[b][e];
-      return fast_exp2(fmaf(s[b][n][2 * e + k], sl, -mu));
+      return fast_exp2(fmaf(s[b][n][2 * e + k], sl, -m[b][e]));
     };
     auto split = [&](int b, int i, float p0, float p1) {
       const uint32_t h = pack_bf16x2(p0, p1);
@@ -234,7 +233,8 @@ struct WarpRows {
         ls[b][e] = 0.f;
 #pragma unroll
         for (int n = 0; n < 2; ++n) {
-          // (an offset of -inf, no key seen yet, makes x +inf: done again)
+          // (kNoOffset, no finite score seen yet, makes the exponential of a
+          // finite score infinite: done again)
           const float x0 = fmaf(s[b][n][2 * e], sl, -m[b][e]);
           const float x1 = fmaf(s[b][n][2 * e + 1], sl, -m[b][e]);
           top = fmax3(top, x0, x1);

@@ -724,7 +724,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                             ? first_limit + (real ? t * per + qi : tb - 1)
                             : u.b.key_end - 1;
       const int tile_limit = kCausal ? first_limit + t * per : limit;
-      float m_run = -INFINITY, l_run = 0.f;
+      float m_run = kNoOffset, l_run = 0.f;
       // ---- the halves: two loads of 32 columns, the second in flight while the
       //      first is exponentiated against the offset m_run as it stands, the
       //      maximum beside it.  Halves with hidden keys, the first of a unit
@@ -835,7 +835,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               tmem_wait32(x);
               tmem_wait32(y);
             }
-            m_use = m_run == -INFINITY ? 0.f : m_run;
+            m_use = m_run;
             sum = make_float2(0.f, 0.f);
 #pragma unroll
             for (int e = 0; e < 32; ++e) {
@@ -862,7 +862,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (n > 0 && ok) ok = o_ready();
       const bool any = n > 0 && ok;
       if (!any) {
-        m_run = -INFINITY;
+        m_run = kNoOffset;
         l_run = 0.f;
       }
       if (!wait_warp(&sm.clean[ub], (round >> 1) & 1)) ok = false;

@@ -7,6 +7,12 @@
 
 namespace tv {
 
+// The running offset of a row that has seen no finite score: the lowest finite
+// number.  Any finite score exceeds it, and a score of minus infinity (an infinity
+// in K) against it is weight 0; against an offset of minus infinity it would be
+// NaN.
+constexpr float kNoOffset = -3.402823466e38f;
+
 // The key tiles of a block, from the rows it covers.
 struct TileBlock {
   int q_row;            // first query row in q / out

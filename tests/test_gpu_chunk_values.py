@@ -1,11 +1,12 @@
-"""Values of chunk and cross attention where the weights themselves show."""
+"""Values of chunk and cross attention where the weights themselves show: two
+keys that nearly cancel, and keys whose scores are minus infinity."""
 import numpy as np
 import pytest
 import torch
 
 import oracle
 import serving_util as U
-from gpu_util import bf16_bits, err_word, require_gpu, upload
+from gpu_util import (assert_parity, bf16_bits, err_word, require_gpu, upload)
 from paged_kv_cache_376_b200 import _lib
 from paged_kv_cache_376_b200 import workloads as W
 
@@ -90,6 +91,34 @@ def test_two_keys_that_nearly_cancel(rows, causal):
         got = W.bf16_to_f64(bf16_bits(_run(wl, causal, ws)))
         off = np.abs(got - ref) / bound
         assert (off <= 1).all(), (ws, off.max(), (off > 1).mean())
+
+
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("rows,lens,hidden", [
+    (4, [600, 100], [200, 64]),        # 16 rows x heads: no padded row
+    (8, [600, 130], [300, 90]),        # 32
+    (3, [600, 100], [200, 64]),        # padded
+    (70, [900, 400], [400, 130]),      # the tile kernel
+    (8, [30000, 70], [14000, 20]),     # cut along the keys: parts without
+    (70, [30000, 200], [14000, 64]),   # any finite score
+], ids=["16", "32", "padded", "tiles", "cut", "cut tiles"])
+def test_scores_of_minus_infinity_come_before_the_first_finite(rows, lens,
+                                                               hidden, causal):
+    """An infinity in K gives scores of minus infinity: weight zero, as long as
+    some key of the row has a finite score.  What comes first in the context
+    must make no difference."""
+    wl = U.cross_workload(lens, [rows] * 2, 802, num_q_heads=8, num_kv_heads=2)
+    q = W.bf16_to_f64(wl.q)
+    q[..., 0] = np.abs(q[..., 0]) + 0.25
+    wl.q = _bits(q)
+    k = W.bf16_to_f64(wl.k_pool)
+    for s, n in enumerate(hidden):
+        for j in range(n):
+            k[_slot(wl, s, j)][:, 0] = -np.inf
+    wl.k_pool = _bits(k)
+    ref = _oracle(wl, causal)
+    for ws in (False, True):
+        assert_parity(_run(wl, causal, ws), ref, f"workspace={ws}")
 
 
 @pytest.mark.parametrize("causal", [True, False])
