@@ -821,6 +821,8 @@ def tv_page_copy(k_pool, v_pool, src_pages, dst_pages, num_pairs=None,
     if v_pool.shape != k_pool.shape or src_pages.dim() != 1 or \
             src_pages.shape != dst_pages.shape:
         raise ValueError("shape mismatch")
+    if num_pairs is not None and num_pairs.numel() < 1:
+        raise ValueError("num_pairs must be [1]")   # none would mean all pairs
     num_pages, ps, hkv, d = k_pool.shape
     dev, st = _one_device((k_pool, v_pool, src_pages, dst_pages, num_pairs,
                            err), stream)

@@ -47,11 +47,16 @@ struct Call {
     return contiguous(o, at::kBFloat16);
   }
   const at::Tensor* ints(PyObject* o) { return contiguous(o, at::kInt); }
-  // pointer of an optional tensor
+  // pointer of an optional tensor (one without elements has none, which must
+  // not pass for None)
   void* maybe(PyObject* o, at::ScalarType type) {
     if (o == Py_None) return nullptr;
     const at::Tensor* t = contiguous(o, type);
-    return t ? t->data_ptr() : nullptr;
+    if (!t || t->numel() == 0) {
+      ok = false;
+      return nullptr;
+    }
+    return t->data_ptr();
   }
   void need(bool condition) { ok = ok && condition; }
   // the launch goes to the current device's current stream
