@@ -9,6 +9,8 @@ eager fallback: without the built library every call raises.
 from __future__ import annotations
 
 import ctypes
+import importlib.machinery
+import importlib.util
 import os
 
 import torch
@@ -113,10 +115,28 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
         fn.restype = res
         fn.argtypes = args
     global _fast
-    from . import _fastcall
-    _fast = _fastcall
+    _fast = _load_fast() if os.path.samefile(path, LIB_PATH) else None
     _lib = lib
     return lib
+
+
+def _load_fast():
+    """The C++ side of the ordinary calls, which calls the package's libtv.so;
+    None where it is not built for this torch and interpreter (the calls here
+    then make every check themselves)."""
+    from .build import fast_path
+    path = fast_path()
+    if not os.path.exists(path):
+        return None
+    name = __package__ + "._fastcall"
+    loader = importlib.machinery.ExtensionFileLoader(name, path)
+    try:
+        module = importlib.util.module_from_spec(
+            importlib.util.spec_from_loader(name, loader))
+        loader.exec_module(module)
+    except ImportError:
+        return None
+    return module
 
 
 def _check(status: int, what: str) -> None:

@@ -13,13 +13,13 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB_PATH = os.path.join(PKG, "libtv.so")
-FAST_PATH = os.path.join(PKG, "_fastcall.so")
 FAST_SOURCE = os.path.join(CSRC, "fastcall.cpp")
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 
@@ -48,15 +48,32 @@ def up_to_date() -> bool:
     return all(os.path.getmtime(p) <= t for p in _inputs())
 
 
-def _build_fastcall(verbose: bool = False) -> None:
-    """_fastcall.so: the C++ side of _lib's ordinary calls (torch's headers,
-    libtv's C calls)."""
-    import sysconfig
-
+def fast_path() -> str:
+    """Where the C++ side of the binding for this torch and this interpreter
+    is: it is made of both's C++, and fits no other."""
     import torch
+    return os.path.join(PKG, f"_fastcall-{sysconfig.get_config_var('SOABI')}"
+                             f"-torch{torch.__version__}.so")
+
+
+def fast_up_to_date() -> bool:
+    path = fast_path()
+    if not os.path.exists(path):
+        return False
+    t = os.path.getmtime(path)
+    return all(os.path.getmtime(p) <= t for p in (
+        FAST_SOURCE, os.path.join(INCLUDE, "tv.h"),
+        os.path.join(PKG, "build.py")))
+
+
+def _build_fastcall(verbose: bool = False) -> None:
+    """The C++ side of _lib's ordinary calls (torch's headers, libtv's C
+    calls)."""
+    import torch
+    path = fast_path()
     root = os.path.join(os.path.dirname(torch.__file__))
     inc = os.path.join(root, "include")
-    tmp = FAST_PATH + f".tmp{os.getpid()}"
+    tmp = path + f".tmp{os.getpid()}"
     cuda = os.path.dirname(os.path.dirname(os.path.realpath(_nvcc())))
     cmd = [shutil.which("g++") or "g++", "-O2", "-std=c++17", "-fPIC",
            "-shared",
@@ -71,14 +88,12 @@ def _build_fastcall(verbose: bool = False) -> None:
     if verbose:
         print(" ".join(cmd), flush=True)
     subprocess.run(cmd, check=True)
-    os.replace(tmp, FAST_PATH)
+    os.replace(tmp, path)
 
 
 def build(force: bool = False, verbose: bool = False) -> str:
     _build_lib(force, verbose)
-    need = [FAST_SOURCE, os.path.join(INCLUDE, "tv.h")]
-    if force or not os.path.exists(FAST_PATH) or any(
-            os.path.getmtime(p) > os.path.getmtime(FAST_PATH) for p in need):
+    if force or not fast_up_to_date():
         _build_fastcall(verbose)
     return LIB_PATH
 
