@@ -49,7 +49,8 @@
  *       TV_DEVERR_BAD_CONTEXT  context_len < 0 or > max_blocks * page_size;
  *                              clamped into range
  *       TV_DEVERR_TIMEOUT      a bounded internal wait (2 s) ran out; the
- *                              affected outputs are zeros
+ *                              affected outputs are zeros (of tv_paged_decode
+ *                              and its variants: not to be used)
  *       TV_DEVERR_BAD_QUERY    query_start_loc inconsistent with the context
  *       TV_DEVERR_POOL_EMPTY   the page pool had too few free pages for a
  *                              sequence (tv_pool_append_slots)

@@ -340,7 +340,9 @@ struct WarpRows {
 struct Joined {
   float M = -INFINITY, L = 0.f;
   float4 x = make_float4(0.f, 0.f, 0.f, 0.f), y = x;
+  bool lost = false;    // a part of it ran out of time: zeros
   __device__ __forceinline__ void add(float m, float l, float4 u, float4 v) {
+    lost |= m != m;     // (an offset is NaN only as this mark)
     // equal offsets first: -inf (no finite score) must not become NaN
     const float f = m == M ? 1.f : fast_exp2(m - M);
     L = fmaf(l, f, L);
@@ -363,11 +365,15 @@ struct Joined {
   }
   __device__ __forceinline__ void write(__nv_bfloat16* row, int k) const {
     const float inv = L == 0.f ? 0.f : 1.f / L;   // NaN scores stay NaN
-    *reinterpret_cast<uint2*>(row + 4 * k) = make_uint2(
-        pack_bf16x2(x.x * inv, x.y * inv), pack_bf16x2(x.z * inv, x.w * inv));
-    *reinterpret_cast<uint2*>(row + 32 + 4 * k) = make_uint2(
-        pack_bf16x2(y.x * inv, y.y * inv), pack_bf16x2(y.z * inv, y.w * inv));
+    uint2 lo = make_uint2(pack_bf16x2(x.x * inv, x.y * inv),
+                          pack_bf16x2(x.z * inv, x.w * inv));
+    uint2 hi = make_uint2(pack_bf16x2(y.x * inv, y.y * inv),
+                          pack_bf16x2(y.z * inv, y.w * inv));
+    if (lost) lo = hi = make_uint2(0, 0);
+    *reinterpret_cast<uint2*>(row + 4 * k) = lo;
+    *reinterpret_cast<uint2*>(row + 32 + 4 * k) = hi;
   }
+  __device__ __forceinline__ float mark() const { return lost ? NAN : M; }
 };
 
 template <int kW>
@@ -528,7 +534,8 @@ __global__ void __launch_bounds__(kThreads, 3)
     }
     const bool page_ok = __shfl_sync(0xffffffffu, cur, i & 31) >= 0;
     if (!__all_sync(0xffffffffu, mbar_wait(smem_u32(&sm.full[warp][stage]),
-                                           (i / kStages) & 1))) {
+                                           (i / kStages) & 1)) ||
+        TV_GIVE_UP(0, warp, i)) {
       failed = true;
       break;
     }
@@ -547,12 +554,13 @@ __global__ void __launch_bounds__(kThreads, 3)
     }
   }
   if (failed) {
-    // let the copies in flight land (bounded), then an empty result
+    // let the copies in flight land (bounded)
     if (lane == 0) flag_error(a.err, DEVERR_TIMEOUT);
     for (int k = i; k < issued; ++k)
       mbar_wait(smem_u32(&sm.full[warp][k % kStages]), (k / kStages) & 1);
-    rows.clear();
   }
+  // the rows need every warp's keys: without one warp's they are zeros
+  if (__syncthreads_or(failed)) rows.clear();
 
   // ---- combine the four warps, 16 rows at a time, and write -----------------------
   rows.finish_sums();
@@ -612,6 +620,7 @@ struct BalancedSmem {
   int32_t warp_total[kW + 1];
   int32_t items;
   int32_t last[2];
+  int32_t failed;              // a warp's wait ran out
   uint32_t bad[kW][kStages];   // the slot's block was no page
   int32_t pre[kMaxChunkSeqs + 1];
 };
@@ -654,7 +663,22 @@ template <bool kCausal>
 __device__ __forceinline__ void join_tiles(const ChunkArgs& a, int warp,
                                            int warps, int lane) {
   const int Hkv = a.num_kv_heads;
-  const int tasks = __ldcg(&a.plan->joins) * Hkv * 2 * 4 * 8;
+  const int2 end = __ldcg(reinterpret_cast<const int2*>(&a.plan->joins));
+  if (end.y) {
+    // a wait of the tile kernel ran out, and units may have been left: the rows
+    // of all its sequences are zeros
+    for (int s = warp; s < a.num_seqs; s += warps) {
+      TileBlock b;
+      if (!tile_block<kCausal>(a, s, 0, &b)) continue;
+      const int64_t n =
+          (int64_t)(a.query_start_loc[s + 1] - b.q_row) * a.num_q_heads * 8;
+      uint4* row = reinterpret_cast<uint4*>(
+          a.out + (size_t)b.q_row * a.num_q_heads * kD);
+      for (int64_t i = lane; i < n; i += 32) row[i] = make_uint4(0, 0, 0, 0);
+    }
+    return;
+  }
+  const int tasks = end.x * Hkv * 2 * 4 * 8;
   for (int i = warp; i < tasks; i += warps) {
     const int dims = i & 7, quarter = (i >> 3) & 3, t = (i >> 5) & 1;
     const int kvh = (i >> 6) % Hkv;
@@ -721,7 +745,7 @@ __global__ void __launch_bounds__((compute_warps(MB) + 1) * 32,
   const int Hkv = a.num_kv_heads;
 
   // ---- blocks per sequence, exclusive prefix in shared memory ------------------
-  if (threadIdx.x == 0) sm.items = 0;
+  if (threadIdx.x == 0) sm.items = sm.failed = 0;
   if (lane == 0 && warp < kW) {
     for (int s = 0; s < kStages; ++s) {
       mbar_init(smem_u32(&sm.ring.full[warp][s]), 1);
@@ -904,7 +928,8 @@ __global__ void __launch_bounds__((compute_warps(MB) + 1) * 32,
       for (; x < end && !failed; x += kW) {
         if (!__all_sync(0xffffffffu,
                         mbar_wait(smem_u32(&sm.ring.full[warp][stage]),
-                                  parity))) {
+                                  parity)) ||
+            TV_GIVE_UP(1, warp, x - x0)) {
           failed = true;
           break;
         }
@@ -919,7 +944,7 @@ __global__ void __launch_bounds__((compute_warps(MB) + 1) * 32,
           parity ^= 1;
         }
       }
-      if (failed) rows.clear();
+      if (failed) sm.failed = 1;
       if (end < x1) {   // the next q, in flight during the combine
         set_rows();
         rows.load(a, w, head, lane);
@@ -929,12 +954,17 @@ __global__ void __launch_bounds__((compute_warps(MB) + 1) * 32,
       rows.finish_sums();
       const bool whole = p0 == base && end == sm.pre[seq + 1];
       const int slot = p0 == x0 ? 0 : 1;
+      bool lost = false;
       float* part =
           a.ws_parts + ((size_t)blockIdx.x * 2 + slot) * kChunkPartFloats;
 #pragma unroll
       for (int b = 0; b < MB; ++b) {
         if (16 * b >= n_rows) break;
         compute_barrier<kW>();   // the last rows have been read
+        // the rows need every warp's keys: without one warp's, here or in a
+        // part of theirs elsewhere, they are zeros
+        if (b == 0) lost = *(volatile int32_t*)&sm.failed != 0;
+        if (lost) rows.clear();
         rows.put(sm.cb, b, warp, lane);
         compute_barrier<kW>();
         const int row = 16 * b + r16;
@@ -948,7 +978,7 @@ __global__ void __launch_bounds__((compute_warps(MB) + 1) * 32,
           __stcg(dst, j.x);
           __stcg(dst + 8, j.y);
           if (k8 == 0) {
-            __stcg(part + row, j.M);
+            __stcg(part + row, lost ? NAN : j.M);
             __stcg(part + kChunkPartRows + row, j.L);
           }
         }
@@ -1042,7 +1072,7 @@ __global__ void __launch_bounds__((compute_warps(MB) + 1) * 32,
               for (int e = 0; e < 8; ++e) j.add(m8[e], l8[e], x8[e], y8[e]);
             }
             if (k8 == 0) {
-              sm.cb.m[warp][g + jr] = j.M;
+              sm.cb.m[warp][g + jr] = j.mark();
               sm.cb.l[warp][g + jr] = j.L;
             }
             float* acc = sm.cb.acc[warp][g + jr];

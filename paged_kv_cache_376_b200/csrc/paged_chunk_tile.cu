@@ -172,6 +172,7 @@ __global__ void __launch_bounds__(kPlanThreads, 1)
   if (threadIdx.x == kPlanThreads - 1) {
     a.plan->entries = start + sum;
     a.plan->next = a.tile_ctas;
+    a.plan->failed = 0;
   }
   __syncthreads();
   for (int i = threadIdx.x; i < n_items; i += kPlanThreads) {
@@ -302,6 +303,11 @@ __device__ __forceinline__ void issue_pv(uint32_t d, uint32_t p, uint32_t v,
                    kIdescPV, accumulate || i > 0);
 }
 
+// A wait ran out: the kernel that follows then writes zeros.
+__device__ __forceinline__ void give_up(const ChunkArgs& a) {
+  flag_error(a.err, DEVERR_TIMEOUT);
+  a.plan->failed = 1;
+}
 __device__ __forceinline__ bool wait_warp(uint64_t* bar, uint32_t parity) {
   return __all_sync(0xffffffffu, mbar_wait(smem_u32(bar), parity));
 }
@@ -471,6 +477,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const CUtensorMap* tmap = is_v ? &tm_v : &tm_k;
     bool ok = true;
     uint32_t it = 0;
+    int q_loads = 0;
     int unit = blockIdx.x;
     for (int round = 0;; ++round) {
       const int ub = round & 1;
@@ -490,6 +497,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       // the number after this one, fetched while this unit loads
       if (lane == 0) unit = atomicAdd(&a.plan->next, 1);
       sm.poison[ub][lane] = sm.poison[ub][lane + 32] = INT32_MAX;
+      q_loads = round + 1;
       if (lane == 0) {
         const uint32_t qbar = smem_u32(&sm.q_full[ub]);
         mbar_arrive_expect_tx(qbar, 2 * kBM * kRowBytes);
@@ -562,12 +570,15 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (lane == 0) mbar_arrive(smem_u32(&sm.clean[ub]));
       unit = __shfl_sync(0xffffffffu, unit, 0);
     }
-    if (!ok && lane == 0) flag_error(a.err, DEVERR_TIMEOUT);
+    if (!ok && lane == 0) give_up(a);
     // no copy may be in flight when the CTA ends (bounded waits; all of them
     // have landed unless a wait gave up)
-    if (!ok)
+    if (!ok) {
       for (uint32_t i = it > kST ? it - kST : 0; i < it; ++i)
         mbar_wait(smem_u32(&sm.kv_full[i % kST]), (i / kST) & 1);
+      for (int i = max(0, q_loads - 2); i < q_loads; ++i)
+        mbar_wait(smem_u32(&sm.q_full[i & 1]), (i >> 1) & 1);
+    }
   } else if (warp < 4) {
     // ======================= MMA issuers =======================================
     const bool leader = elect_one();
@@ -681,7 +692,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncwarp();
       }
     }
-    if (!ok && lane == 0) flag_error(a.err, DEVERR_TIMEOUT);
+    if (!ok && lane == 0) give_up(a);
     // this thread's products finish before tensor memory is freed
     if (leader) tc_commit(smem_u32(&sm.drain[warp - 1]));
     __syncwarp();
@@ -738,7 +749,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       volatile const int32_t* bad_unit = &sm.bad_unit[ub];
 #pragma unroll 1
       for (int i = 0; i < halves; ++i) {
-          if (!wait_warp(&sm.s_full[t][h.b], h.parity)) {
+          if (!wait_warp(&sm.s_full[t][h.b], h.parity) ||
+              TV_GIVE_UP(2, warp, i)) {
             ok = false;
             break;
           }
@@ -860,12 +872,12 @@ __global__ void __launch_bounds__(kThreads, 1)
 
       // ---- the unit's result, 32 dims at a time ------------------------------------
       if (n > 0 && ok) ok = o_ready();
+      if (!wait_warp(&sm.clean[ub], (round >> 1) & 1)) ok = false;
       const bool any = n > 0 && ok;
       if (!any) {
         m_run = kNoOffset;
         l_run = 0.f;
       }
-      if (!wait_warp(&sm.clean[ub], (round >> 1) & 1)) ok = false;
       const bool poisoned = sm.poisoned[ub] != 0;
       const int parts = u.e.parts;
       // a part: m, l, then O as [dim / 4][row] float4, so that a warp's
@@ -928,7 +940,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       __syncwarp();
       if (lane == 0) mbar_arrive(smem_u32(&sm.q_empty[ub]));
     }
-    if (!ok && lane == 0) flag_error(a.err, DEVERR_TIMEOUT);
+    if (!ok && lane == 0) give_up(a);
   }
 
   tc_fence_before();

@@ -23,7 +23,16 @@ enum : uint32_t {
   DEVERR_BAD_QUERY = 1u << 4,    // query_start_loc inconsistent with context
 };
 
-constexpr unsigned long long kWaitLimitNs = 2000000000ull;  // 2 s
+#ifndef TV_WAIT_LIMIT_NS
+#define TV_WAIT_LIMIT_NS 2000000000ull   // 2 s
+#endif
+constexpr unsigned long long kWaitLimitNs = TV_WAIT_LIMIT_NS;
+// For a test of what follows a wait that ran out: a build that defines it has
+// one met wait of a chunk kernel (0: one CTA per row block, 1: balanced, 2:
+// tiles) count as run out.  Nothing is waited for less.
+#ifndef TV_GIVE_UP
+#define TV_GIVE_UP(kernel, warp, step) false
+#endif
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 

@@ -259,6 +259,8 @@ struct ChunkPlan {
   int32_t entries;
   int32_t next;                  // unit (entry x KV head) to be taken next
   int32_t joins;                 // cut blocks
+  int32_t failed;                // a wait of the tile kernel ran out (read
+                                 // with `joins`)
 };
 struct ChunkArgs {
   __nv_bfloat16* out;            // [rows][Hq][D]
