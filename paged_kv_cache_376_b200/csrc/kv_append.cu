@@ -107,9 +107,9 @@ __global__ void __launch_bounds__(256)
 // whose two lookups depend on one another.  Two head vectors a lane in flight at
 // 64 registers: 8192 tokens of 32 + 16 heads 16.7 us (6.1 TB/s; three at 80
 // registers, fewer warps: 18.7), 64 tokens 4.2 us.
-template <int kHeads>   // heads of a lane in flight at once
 __global__ void __launch_bounds__(128, 8)
     kv_append_mrope_kernel(const MropeArgs a) {
+  constexpr int kHeads = 2;   // heads of a lane in flight at once
   const int lane = threadIdx.x & 31;
   const int u = lane & 3;
   const int heads = a.num_q_heads + 2 * a.num_kv_heads;
@@ -181,8 +181,7 @@ cudaError_t launch_kv_append_mrope(const MropeArgs& a, cudaStream_t stream) {
   if (a.num_tokens == 0) return cudaSuccess;
   const int64_t want = (a.num_tokens + 3) / 4;
   const int64_t cap = (int64_t)device_sm_count() * 64;
-  kv_append_mrope_kernel<2>
-      <<<(int)(want < cap ? want : cap), 128, 0, stream>>>(a);
+  kv_append_mrope_kernel<<<(int)(want < cap ? want : cap), 128, 0, stream>>>(a);
   return cudaGetLastError();
 }
 

@@ -9,10 +9,13 @@
 //
 // What bounds it: a sequence's K and V are read once for up to 32 rows x heads
 // per KV head, and that stream from HBM is the floor.  Up to 16 rows it is also
-// the bound (8 x 131072 tokens, 16 rows: 322 us, 6.7 TB/s); with 32 a warp's
-// step of 1060 clocks a page, a chain of products, exponentials and products
-// with 2.5 warps per scheduler to hide it, takes longer than the page's bytes
-// (64 x 2048 tokens: 64 us, where the stream takes 41).
+// the bound (8 x 131072 tokens, 16 rows: 326 to 343 us on two GPUs, 6.6 to 6.3
+// TB/s, about the rate of a copy).
+// With 32 (64 x 2048 tokens: 70 us, where the stream takes 41) neither the
+// stream, the tensor pipe (36 %) nor the issue slots (38 %) are full: chains of
+// products, exponentials and products on 2.5 warps per scheduler, and 2.7
+// sequences a CTA to combine or to leave a part of; what each of them takes was
+// not measured.
 //
 // Design.  Every warp works on pages of its own, which reach it through a
 // private ring of TMA boxes (16 tokens x 128 B of K and of V, 128-byte
@@ -598,14 +601,19 @@ __global__ void __launch_bounds__(kThreads, 3)
 // blocks up and issues the loads into their rings.  The rings run across
 // sequence ends: the loads of the next sequence are in flight while the last
 // one's warps are combined.  (With each warp issuing its own loads, that took
-// it 670 of the 2370 clocks of a page of 32 rows.)  64 x 2048 tokens, 32 rows:
-// one CTA per sequence and KV head 74 us (512 CTAs on 444 places), this 64;
-// 8 x 131072: 1172 and 322.
+// it 72 us instead of 64 for 64 x 2048 tokens, 32 rows, when P still had one
+// term.)  Measured against one CTA per sequence and KV head, in a graph: 32 rows,
+// 64 x 2048 tokens 68 us and 75 (512 CTAs on 444 places); 16 rows, 8 x 131072: 319
+// and 1196; one row, 8 x 16384: 49 and 143.  Where sequences x KV heads fill the
+// GPU evenly it loses: one row, 64 x 2048 tokens 51 and 44, 64 x 375-1500 states
+// of 16 KV heads 45 and 39.  Every call with a workspace takes it all the same
+// (lengths are on the device, where a rule could not choose the launch); a caller
+// that knows them passes no workspace.
 constexpr int kSnap = 4;
 // A sub-core's 16,384 registers hold three warps of 32 rows (168 each) or four
-// of 16 rows (128) nearly without spills.  Measured, W x CTAs an SM: 32 rows,
-// 64 x 2048 tokens, 5 x 2 64.8 us, 3 x 3 66.6; 16 rows, 8 x 131072 tokens, 4 x 3
-// 322 us, 5 x 2 329, 3 x 3 333.
+// of 16 rows (128) nearly without spills.  Measured with one term of P, W x CTAs
+// an SM: 32 rows, 64 x 2048 tokens, 5 x 2 64.8 us, 3 x 3 66.6; 16 rows,
+// 8 x 131072 tokens, 4 x 3 322 us, 5 x 2 329, 3 x 3 333.
 __host__ __device__ constexpr int compute_warps(int mb) {
   return mb == 1 ? 4 : 5;
 }

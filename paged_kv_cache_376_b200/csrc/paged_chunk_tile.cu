@@ -15,8 +15,11 @@
 // counted twice for P's two terms, and 1024 of the other.  What it takes longer
 // is the softmax warps' own latency: two warps per scheduler are what tensor
 // memory (S, P and O of two query tiles) and registers leave room for (four at
-// 96 registers: slower, they spill).  32 decoder prompts over 1500 states: 188
-// us (339 TFLOP/s, plan and launches included), 162 with P in bf16 alone.  Every
+// 96 registers: slower, they spill).  32 decoder prompts over 1500 states: 185
+// us (345 TFLOP/s, plan and launches included), 162 with P in bf16 alone; in the
+// kernel the tensor pipe is at 35 %, the special function units at 47 %, the
+// issue slots at 44 %.  16 prompts of 512 rows over 2048 keys: 237 us, 229 with
+// tv_paged_prefill.  Every
 // fourth pair of exponentials as a polynomial on the FMA units gains 1 % beside
 // P's two terms (187.3 against 185.3 us) and was left out: a row's bits would
 // depend on which way its neighbours' offsets send the warp.
