@@ -674,7 +674,8 @@ __global__ void __launch_bounds__(kThreads, G <= 4 ? 4 : 2)
 
 // Four CTAs of G <= 4 must fit in one SM's 228 KB (1 KB of it reserved per
 // CTA) so that 16 warps stream per SM.
-static_assert(4 * (sizeof(BalancedSmem) + 1024 + 1024) <= 228 * 1024,
+static_assert(kMaxDecodeCtasPerSm * (sizeof(BalancedSmem) + 1024 + 1024) <=
+                  228 * 1024,
               "shared memory of the balanced decode exceeds 4 CTAs per SM");
 
 template <int G, bool kAppend>

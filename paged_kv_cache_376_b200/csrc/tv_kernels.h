@@ -107,6 +107,7 @@ struct DecodeArgs {
 // Work-balanced decode (paged_decode_balanced.cu).
 constexpr int kMaxBalancedSeqs = 512;    // prefix sums live in shared memory
 constexpr int kMinPagesPerWarp = 4;      // smallest range a warp is given
+constexpr int kMaxDecodeCtasPerSm = 4;   // of four warps each
 constexpr int kSlotFloats = 16 + 8 * 64; // m[8], l[8], acc[8][64] per segment
 
 int balanced_decode_ctas_per_sm(int group, bool append);

@@ -58,4 +58,4 @@ def test_one_decode_workspace_for_every_batch():
         np.testing.assert_array_equal(bf16_bits(out),
                                       first.setdefault(name, bf16_bits(out)))
         sms = torch.cuda.get_device_properties(0).multi_processor_count
-        assert int(ws[:4 * 64 * sms].count_nonzero()) == 0, name
+        assert int(ws[:4 * 16 * sms].count_nonzero()) == 0, name
